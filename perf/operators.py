@@ -1,0 +1,422 @@
+"""Cases of the paged device cache: block plan, row write and read, window attention.
+
+A request's cache of MLA rows (576 elements: latent 512, which is also the value, and rope
+key 64) lives on the device in blocks of `block_tokens` rows reached through a block table,
+in 16 bits or in 4 (E2M1 codes, one E4M3 scale per 16 elements).  `run` computes an operator
+in elementary torch operations, or, with `own`, through the library's entry points.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+ROW, VAL, GROUP = 576, 512, 16
+SCALE = 1.0 / math.sqrt(192.0)
+OK, ERANGE, ECAPACITY = 0, -3, -6
+FORMATS = {"bf16": 0, "q4": 1}
+
+
+def _device():
+    return torch.device("cuda" if torch.cuda.is_available() else "cpu")
+
+
+def listed():
+    return [
+        # a decode step's tables: one new token for each of 16 requests (the 16-request workload)
+        dict(name="plan_decode_16", op="plan", requests=16, context=32768, new=1, ragged=False, ended=False,
+             block=64, window=0, sinks=0),
+        # a server's mixed step: 509 windowed requests, some chunks of prompt, most one token, some over
+        dict(name="plan_mixed_509", op="plan", requests=509, context=16384, new=61, ragged=True, ended=True,
+             block=16, window=4096, sinks=64),
+        # a decode step's new rows (32 requests of 4 positions) into the 4-bit cache, and read back
+        dict(name="rows_q4_128", op="rows", rows=128, block=64, format="q4"),
+        # a prompt chunk's rows with padding behind it, 4 bits, odd count
+        dict(name="rows_q4_65531", op="rows", rows=65531, block=64, format="q4"),
+        # one short request, 16 heads: latency
+        dict(name="one_4k_h16", op="attend", format="bf16", requests=1, context=4096, new=1, ragged=False,
+             heads=16, window=0, sinks=0, block=64),
+        # the 32-request decode batch with a tensor-parallel share of the heads, whole context
+        dict(name="decode_32x32k_h16", op="attend", format="bf16", requests=32, context=32768, new=1, ragged=True,
+             heads=16, window=0, sinks=0, block=64),
+        # four positions of 128 heads over a window and sinks
+        dict(name="window_16x4_h128", op="attend", format="bf16", requests=16, context=32768, new=4, ragged=False,
+             heads=128, window=4096, sinks=64, block=128),
+        # a 4096-token prompt chunk, windowed layer, odd heads
+        dict(name="chunk_4096_h20", op="attend", format="bf16", requests=1, context=16384, new=4096, ragged=False,
+             heads=20, window=1024, sinks=4, block=64),
+        # a few ragged requests over the 4-bit cache: latency
+        dict(name="q4_5x700_h24", op="attend", format="q4", requests=5, context=700, new=2, ragged=True,
+             heads=24, window=0, sinks=0, block=16),
+        # the 64k decode batch on the 4-bit cache, 16 heads
+        dict(name="q4_32x64k_h16", op="attend", format="q4", requests=32, context=65536, new=1, ragged=True,
+             heads=16, window=0, sinks=0, block=64),
+        # four positions of 128 heads on the 4-bit cache, whole context
+        dict(name="q4_16x4x8k_h128", op="attend", format="q4", requests=16, context=8192, new=4, ragged=True,
+             heads=128, window=0, sinks=0, block=64),
+        # one very long request on the 4-bit cache, 128 heads
+        dict(name="q4_1x256k_h128", op="attend", format="q4", requests=1, context=262144, new=1, ragged=False,
+             heads=128, window=0, sinks=0, block=128),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["plan", "rows", "attend", "attend", "attend"])
+    block = rng.choice([8, 16, 24, 64, 128])
+    if op == "plan":
+        window = rng.choice([0, _log(rng, 64, 8192)])
+        return dict(op="plan", requests=_log(rng, 1, 509), context=_log(rng, 16, 16384), new=_log(rng, 1, 61),
+                    ragged=rng.random() < 0.7, ended=rng.random() < 0.5, block=max(block, 16), window=window,
+                    sinks=rng.choice([0, 4, 64]))
+    if op == "rows":
+        return dict(op="rows", rows=_log(rng, 1, 65531), block=block, format=rng.choice(["q4", "q4", "bf16"]))
+    while True:
+        c = dict(op="attend", format=rng.choice(["bf16", "q4"]), requests=_log(rng, 1, 64), context=_log(rng, 16, 262144),
+                 new=1 if rng.random() < 0.4 else _log(rng, 1, 2048), ragged=rng.random() < 0.6, heads=_log(rng, 1, 128),
+                 window=rng.choice([0, 0, _log(rng, 32, 8192)]), sinks=rng.choice([0, 4, 64]), block=block)
+        c["context"] = max(c["context"], c["new"])
+        span = _span(c)
+        if (work(c)["flops"] <= 2.5e11 and c["requests"] * c["context"] <= (1 << 21) and c["requests"] * span <= (1 << 20)
+                and c["requests"] * c["new"] * c["heads"] * span <= (1 << 29)):
+            return c
+
+
+def _span(c):
+    """Rows of the cache that a request's positions can see, at most."""
+    return min(c["context"], c["window"] + c["sinks"] + c["new"]) if c["window"] else c["context"]
+
+
+# ---- inputs ---------------------------------------------------------------------------------
+
+def _lengths(c):
+    """(cached lengths with the new tokens, new tokens) of each request: the case's alone."""
+    R = c["requests"]
+    g = np.random.default_rng([R, c["context"], c["new"]])
+    kv = np.full(R, c["context"], np.int64)
+    new = np.full(R, c["new"], np.int64)
+    if c["ragged"]:
+        kv = np.maximum(1, (kv * g.uniform(0.4, 1.0, R)).astype(np.int64))
+        new = np.maximum(1, (new * g.uniform(0.3, 1.0, R)).astype(np.int64))
+        kv[0], new[0] = c["context"], c["new"]
+    return np.maximum(kv, new), new
+
+
+def _values(i):
+    """E2M1 codes (0..15) -> values."""
+    t = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0],
+                     dtype=torch.float32, device=i.device)
+    return t[i.long()]
+
+
+def _quantize(rows):
+    """Rows [n][576] -> (codes [n][36][16] uint8, scales [n][36] float32, values of E4M3)."""
+    x = rows.float().view(-1, ROW // GROUP, GROUP)
+    s = (x.abs().amax(-1) / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn).float()
+    a = x.abs() / torch.where(s > 0, s, torch.ones_like(s))[..., None]
+    a = torch.where((s > 0)[..., None], a, torch.zeros_like(a))
+    m = ((a > 0.25).byte() + (a >= 0.75).byte() + (a > 1.25).byte() + (a >= 1.75).byte() + (a > 2.5).byte()
+         + (a >= 3.5).byte() + (a > 5.0).byte())
+    return m | ((x < 0).byte() << 3), s
+
+
+def _pack(codes, scales, block):
+    """The 4-bit cache's blocks: codes [block][288] (in each 32-bit word element 2k is nibble k and element
+    2k + 1 nibble k + 4), then scales [block][36]."""
+    n = codes.shape[0]
+    e = codes.reshape(n, ROW // 8, 4, 2)
+    w = torch.cat([e[..., 0::2, 0] | (e[..., 1::2, 0] << 4), e[..., 0::2, 1] | (e[..., 1::2, 1] << 4)], dim=-1)
+    w = w.reshape(n // block, block * ROW // 2)
+    s = scales.to(torch.float8_e4m3fn).view(torch.uint8).reshape(n // block, block * ROW // GROUP)
+    return torch.cat([w, s], dim=1).contiguous()
+
+
+def _unpack(pool, block, at):
+    """float32 rows [.., 576] of the 4-bit cache at slots `at`."""
+    codes = pool[:, :block * ROW // 2].reshape(-1, ROW // 2)[at].view(*at.shape, ROW // 8, 4)
+    scales = pool[:, block * ROW // 2:].reshape(-1, ROW // GROUP)[at].view(torch.float8_e4m3fn).float()
+    e = torch.stack([codes & 15, codes >> 4], dim=-1).reshape(*at.shape, ROW // 8, 2, 4).transpose(-1, -2)
+    v = _values(e.reshape(*at.shape, ROW // GROUP, GROUP)) * scales[..., None]
+    return v.reshape(*at.shape, ROW)
+
+
+def _rows_at(s, at):
+    if s["format"] == "q4":
+        return _unpack(s["pool"], s["block"], at)
+    return s["pool"].view(-1, ROW)[at].float()
+
+
+def prepare(case, seed):
+    c, dev = case, _device()
+    g = np.random.default_rng(seed)
+    tg = torch.Generator(device=dev).manual_seed(seed)
+    if c["op"] == "rows":
+        n, B = c["rows"], c["block"]
+        n_blocks = -(-n // B) + 3
+        slots = torch.from_numpy(g.permutation(n_blocks * B)[:n].astype(np.int32))
+        slots[torch.from_numpy(g.random(n) < 0.02)] = -1  # padding rows
+        rows = torch.randn(n, ROW, generator=tg, device=dev) * torch.exp(torch.randn(n, 1, generator=tg, device=dev))
+        width = 1152 * B if c["format"] == "bf16" else 324 * B
+        return dict(op="rows", format=c["format"], block=B, n_blocks=n_blocks, rows=rows.bfloat16(), slots=slots.to(dev),
+                    pool=torch.zeros(n_blocks, width, dtype=torch.uint8, device=dev))
+    R, B = c["requests"], c["block"]
+    kv, new = _lengths(c)
+    i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(dev)  # noqa: E731
+    if c["op"] == "plan":
+        old = kv - new
+        if c["ended"]:
+            new = np.where(g.random(R) < 0.1, -1, new)
+            new = np.where(g.random(R) < 0.1, 0, new)
+        M = -(-c["context"] // B) + -(-c["new"] // B) + 1
+        table = np.full((R, M), -1, np.int64)
+        held = -(-old // B)
+        n_blocks = int(held.sum() + 3 * R * (c["new"] // B + 2))
+        perm = g.permutation(n_blocks)
+        live = np.arange(M)[None, :] < held[:, None]
+        table[live] = perm[:int(held.sum())]
+        ring = np.full(4 * n_blocks, -1, np.int64)
+        ring[7:7 + n_blocks - int(held.sum())] = perm[int(held.sum()):]
+        return dict(op="plan", lengths=i32(old), new=i32(new), table=i32(table), ring=i32(ring), block=B,
+                    bounds=torch.tensor([7, 7 + n_blocks - int(held.sum())], dtype=torch.int64, device=dev),
+                    window=c["window"], sinks=c["sinks"], n_slots=R * c["new"] + 5, steps=c["new"],
+                    most=-(-c["context"] // B) + 1)
+    M = -(-c["context"] // B) + 2
+    used = -(-kv // B)
+    n_blocks = int(used.sum()) + 2
+    table = np.full((R, M), -1, np.int64)
+    table[np.arange(M)[None, :] < used[:, None]] = g.permutation(n_blocks)[:int(used.sum())]
+    if c["format"] == "bf16":
+        pool = torch.empty(n_blocks, B, ROW, dtype=torch.bfloat16, device=dev)
+    else:
+        pool = torch.empty(n_blocks, 324 * B, dtype=torch.uint8, device=dev)
+    step = max(1, (1 << 17) // B)
+    for a in range(0, n_blocks, step):
+        b = min(n_blocks, a + step)
+        x = torch.randn((b - a) * B, ROW, generator=tg, device=dev).bfloat16()
+        pool[a:b] = x.view(b - a, B, ROW) if c["format"] == "bf16" else _pack(*_quantize(x), B)
+    T = int(new.sum())
+    q = torch.randn(T, c["heads"], ROW, generator=tg, device=dev).bfloat16()
+    return dict(op="attend", format=c["format"], pool=pool, n_blocks=n_blocks, block=B, table=i32(table),
+                kv=i32(kv), cu=i32(np.concatenate([[0], np.cumsum(new)])), q=q, window=c["window"],
+                sinks=c["sinks"], steps=c["new"], span=_span(c), context=c["context"])
+
+
+# ---- the operators --------------------------------------------------------------------------
+
+def run(state):
+    s = state
+    if own:
+        return _own(s)
+    if s["op"] == "plan":
+        return _plan(s)
+    if s["op"] == "rows":
+        return _rows(s)
+    return _attend(s, torch.float32)
+
+
+def _own(s):
+    from top_cache_gb300 import kvo as K
+    dev = s["table"].device if "table" in s else s["rows"].device
+    if s["op"] == "plan":
+        R = s["lengths"].numel()
+        e = lambda n: torch.empty(n, dtype=torch.int32, device=dev)  # noqa: E731
+        out = dict(lengths=e(R), kv_lens=e(R), cu=e(R + 1), slots=e(s["n_slots"]), status=e(R),
+                   bounds=torch.empty(2, dtype=torch.int64, device=dev))
+        K.kvo_paged_plan(s["lengths"], s["new"], s["block"], s["table"], s["ring"], s["bounds"], out["bounds"],
+                         out["lengths"], out["kv_lens"], out["cu"], out["slots"], out["status"],
+                         window=s["window"], sinks=s["sinks"])
+        out["table"], out["ring"] = s["table"], s["ring"]
+        return out
+    if s["op"] == "rows":
+        K.kvo_paged_write(s["rows"], s["slots"], s["pool"], s["n_blocks"], s["block"], FORMATS[s["format"]])
+        back = torch.zeros_like(s["rows"])
+        K.kvo_paged_read(s["pool"], s["n_blocks"], s["block"], FORMATS[s["format"]], s["slots"], back)
+        return back
+    T, H = s["q"].shape[0], s["q"].shape[1]
+    out = torch.empty(T, H, VAL, dtype=torch.bfloat16, device=dev)
+    lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+    K.kvo_paged_attend(s["pool"], s["n_blocks"], s["block"], FORMATS[s["format"]], s["table"], s["kv"], s["cu"],
+                       s["q"], SCALE, out, lse, window=s["window"], sinks=s["sinks"])
+    return out, lse
+
+
+def _plan(s):
+    """Block tables, slots and the ring of free blocks after a step of the given new tokens."""
+    B, W, sb = s["block"], s["window"], -(-s["sinks"] // s["block"])
+    old, n = s["lengths"].long(), s["new"].long()
+    R, M = s["table"].shape
+    F = s["ring"].numel()
+    head, tail = s["bounds"][0], s["bounds"][1]
+    grow = n.clamp(min=0)
+    cu = torch.cat([grow.new_zeros(1), grow.cumsum(0)])
+    have, want = -(-old // B), -(-(old + grow) // B)
+    fits = (want <= M) & (cu[1:] <= s["n_slots"])
+    need = torch.where(fits, want - have, torch.zeros_like(want))
+    cum = need.cumsum(0)
+    served = fits & ((need == 0) | (cum <= tail - head))
+    status = torch.where(fits, torch.where(served, OK, ECAPACITY), ERANGE)
+    dead = lambda L: ((L - W + 1).clamp(min=0) // B).clamp(min=sb) if W > 0 else torch.full_like(L, sb)  # noqa: E731
+    j = torch.arange(M, device=old.device)[None, :]
+    fresh = (j >= have[:, None]) & (j < want[:, None]) & served[:, None]
+    at = (head + (cum - need)[:, None] + j - have[:, None]) % F
+    table = torch.where(fresh, s["ring"].long()[at], s["table"].long())
+    ended = n < 0
+    gone = torch.where(ended[:, None], (j < have[:, None]) & ((j < sb) | (j >= dead(old)[:, None])),
+                       served[:, None] & (j >= dead(old)[:, None]) & (j < torch.minimum(dead(old + grow), want)[:, None]))
+    place = (tail + gone.reshape(-1).long().cumsum(0) - 1) % F
+    ring = torch.cat([s["ring"].long(), s["ring"].new_zeros(1).long()])
+    ring[torch.where(gone.reshape(-1), place, torch.full_like(place, F))] = table.reshape(-1)
+    length = torch.where(ended, torch.zeros_like(old), torch.where(served, old + grow, old))
+    i = torch.arange(s["n_slots"], device=old.device)
+    r = torch.searchsorted(cu[1:], i, right=True).clamp(max=R - 1)
+    t = old[r] + i - cu[r]
+    slot = table[r, (t // B).clamp(max=M - 1)] * B + t % B
+    slot = torch.where((i < cu[R]) & served[r], slot, torch.full_like(slot, -1))
+    used = torch.where(served, need, torch.zeros_like(need)).sum()
+    i32 = lambda x: x.to(torch.int32)  # noqa: E731
+    s["table"].copy_(table)
+    s["ring"].copy_(ring[:F])
+    return dict(lengths=i32(length), kv_lens=i32(torch.where(served, length, torch.zeros_like(length))), cu=i32(cu),
+                slots=i32(slot), status=i32(status), bounds=torch.stack([head + used, tail + gone.sum()]),
+                table=s["table"], ring=s["ring"])
+
+
+def _rows(s):
+    """Rows into the cache at their slots, and the cache's values at those slots."""
+    at = s["slots"].long()
+    keep = (at >= 0)[:, None]
+    if s["format"] == "bf16":
+        x = s["rows"]
+        w = s["pool"].view(torch.bfloat16).view(-1, ROW)
+        w[at.clamp(min=0)] = torch.where(keep, x, w[at.clamp(min=0)])
+    else:
+        codes, scales = _quantize(s["rows"])
+        x = (_values(codes) * scales[..., None]).reshape(-1, ROW).bfloat16()
+    return torch.where(keep, x, torch.zeros_like(x))
+
+
+def _attend(s, dt):
+    """Attention over each position's visible rows, in type dt."""
+    R, B, W, S = s["kv"].numel(), s["block"], s["window"], s["sinks"]
+    dev, span, P = s["q"].device, s["span"], s["steps"]
+    kv, cu = s["kv"].long(), s["cu"].long()
+    new = cu[1:] - cu[:-1]
+    # the rows that a request's positions can see: [sinks |] lo .. kv - 1
+    if span < s["context"]:
+        lo = (kv - new - W + 1).clamp(min=0)
+        x = torch.arange(span, device=dev)[None, :]
+        t = torch.where(x < S, x, (lo[:, None] + x - S))
+        ok = (x < S) | (t >= S)
+    else:
+        t = torch.arange(span, device=dev)[None, :].expand(R, span)
+        ok = torch.ones_like(t, dtype=torch.bool)
+    ok = ok & (t < kv[:, None])
+    t = torch.minimum(t, kv[:, None] - 1).clamp(min=0)
+    slot = s["table"].long().gather(1, t // B) * B + t % B
+    k = _rows_at(s, slot).to(dt)                                             # [R][span][576]
+    i = torch.arange(P, device=dev)[None, :]
+    qi = (cu[:-1, None] + i).clamp(max=s["q"].shape[0] - 1)
+    q = s["q"][qi].to(dt).flatten(1, 2)                                      # [R][P * H][576]
+    H = s["q"].shape[1]
+    pos = kv[:, None] - new[:, None] + i
+    see = ok[:, None, :] & (t[:, None, :] <= pos[..., None])
+    if W > 0:
+        see = see & ((t[:, None, :] > pos[..., None] - W) | (t[:, None, :] < S))
+    z = torch.matmul(q, k.transpose(1, 2)).view(R, P, H, span).mul_(SCALE)
+    z.masked_fill_(~see[:, :, None, :], -math.inf)
+    m = z.amax(-1, keepdim=True).clamp(min=-1e30)
+    z = z.sub_(m).exp_()
+    l = z.sum(-1, keepdim=True)
+    o = torch.matmul(z.view(R, P * H, span), k[..., :VAL]).view(R, P, H, VAL) / torch.where(l > 0, l, torch.ones_like(l))
+    lse = (m + l.log()).squeeze(-1)
+    real = i < new[:, None]
+    o, lse = o[real], lse[real]
+    if dt == torch.float64:
+        return o, lse
+    return o.to(torch.bfloat16), lse
+
+
+def work(case):
+    c = case
+    one = 1152 if c.get("format") == "bf16" else 324
+    if c["op"] == "rows":
+        return {"bytes": c["rows"] * (2 * 1152 + 2 * one + 8.0), "flops": 0.0}
+    R = c["requests"]
+    kv, new = _lengths(c)
+    if c["op"] == "plan":  # in: lengths, new tokens, free blocks; out: tables, slots, four arrays of the requests
+        blocks = (-(-kv // c["block"]) - -(-(kv - new) // c["block"])).sum()
+        return {"bytes": 4.0 * (6 * R + R * c["new"] + 2 * blocks) + 32, "flops": 0.0}
+    W, S = c["window"], c["sinks"]
+    pairs = rows = 0.0
+    for L, n in zip(kv, new):
+        p = np.arange(L - n, L)
+        low = np.maximum(0, p - W + 1) if W else np.zeros_like(p)
+        pairs += (p + 1 - low + np.minimum(S, low)).sum()
+        rows += L - low[0] + min(S, low[0])
+    T = float(new.sum())
+    return {"bytes": rows * one + T * c["heads"] * (1152 + 1024 + 4.0), "flops": 2.0 * (ROW + VAL) * pairs * c["heads"]}
+
+
+# ---- from the definitions, in 64 bits ---------------------------------------------------------
+
+def exact(case, seed):
+    c = case
+    if c["op"] == "plan":
+        return None  # whole numbers only
+    s = prepare(case, seed)
+    if c["op"] == "rows":
+        return _exact_rows(s)
+    if 2.0 * 1088 * c["requests"] * c["new"] * c["heads"] * _span(c) > 6e12:
+        return None  # more than about 20 seconds in 64 bits
+    return _exact_attend(s)
+
+
+def _exact_rows(s):
+    x = s["rows"].double()
+    if s["format"] == "q4":
+        x = x.view(-1, ROW // GROUP, GROUP)
+        # every E4M3 value, and the nearest one (ties to the even code) to max / 6
+        grid = torch.arange(127, dtype=torch.uint8, device=x.device).view(torch.float8_e4m3fn).double()
+        f = _nearest((x.abs().amax(-1) / 6.0).clamp(max=448.0), grid)
+        e2m1 = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64, device=x.device)
+        a = torch.where(f[..., None] > 0, x.abs() / f[..., None], torch.zeros_like(x)).clamp(max=6.0)
+        x = (_nearest(a, e2m1) * f[..., None] * torch.sign(x)).reshape(-1, ROW)
+    return torch.where((s["slots"] >= 0)[:, None], x, torch.zeros_like(x))
+
+
+def _nearest(a, grid):
+    hi = torch.searchsorted(grid, a.contiguous()).clamp(max=grid.numel() - 1)
+    lo = (hi - 1).clamp(min=0)
+    d = (grid[hi] - a) - (a - grid[lo])
+    up = (d < 0) | ((d == 0) & (hi % 2 == 0))
+    return torch.where(up, grid[hi], grid[lo])
+
+
+def _exact_attend(s):
+    """One request and a few positions at a time: the formula over the listed visible rows."""
+    outs, lses = [], []
+    kv, cu = s["kv"].tolist(), s["cu"].tolist()
+    for r in range(len(kv)):
+        t = torch.arange(kv[r], device=s["q"].device)
+        first = kv[r] - (cu[r + 1] - cu[r])
+        W, S = s["window"], s["sinks"]
+        if W:
+            t = t[(t < S) | (t > first - W)]
+        rows = _rows_at(s, s["table"][r].long()[t // s["block"]] * s["block"] + t % s["block"]).double()
+        step = max(1, (1 << 25) // (len(t) * s["q"].shape[1]))
+        for a in range(cu[r], cu[r + 1], step):
+            b = min(cu[r + 1], a + step)
+            z = torch.einsum("phd,td->pht", s["q"][a:b].double(), rows) * SCALE
+            p = (first + torch.arange(a, b, device=t.device) - cu[r])[:, None]
+            hidden = t[None, :] > p
+            if W:
+                hidden = hidden | ((t[None, :] <= p - W) & (t[None, :] >= S))
+            z = z.masked_fill(hidden[:, None, :], -math.inf)
+            lse = torch.logsumexp(z, -1)
+            outs.append(torch.einsum("pht,td->phd", torch.exp(z - lse[..., None]), rows[:, :VAL]))
+            lses.append(lse)
+    return torch.cat(outs), torch.cat(lses)
