@@ -125,21 +125,19 @@ def _quantize(rows):
 
 
 def _pack(codes, scales, block):
-    """The 4-bit cache's blocks: codes [block][288] (in each 32-bit word element 2k is nibble k and element
-    2k + 1 nibble k + 4), then scales [block][36]."""
+    """The 4-bit cache's blocks: codes [block][288] (element 2b in byte b's low four bits, 2b + 1 in its
+    high ones), then scales [block][36]."""
     n = codes.shape[0]
-    e = codes.reshape(n, ROW // 8, 4, 2)
-    w = torch.cat([e[..., 0::2, 0] | (e[..., 1::2, 0] << 4), e[..., 0::2, 1] | (e[..., 1::2, 1] << 4)], dim=-1)
-    w = w.reshape(n // block, block * ROW // 2)
+    e = codes.reshape(n // block, block * ROW // 2, 2)
     s = scales.to(torch.float8_e4m3fn).view(torch.uint8).reshape(n // block, block * ROW // GROUP)
-    return torch.cat([w, s], dim=1).contiguous()
+    return torch.cat([e[..., 0] | (e[..., 1] << 4), s], dim=1).contiguous()
 
 
 def _unpack(pool, block, at):
     """float32 rows [.., 576] of the 4-bit cache at slots `at`."""
-    codes = pool[:, :block * ROW // 2].reshape(-1, ROW // 2)[at].view(*at.shape, ROW // 8, 4)
+    codes = pool[:, :block * ROW // 2].reshape(-1, ROW // 2)[at]
     scales = pool[:, block * ROW // 2:].reshape(-1, ROW // GROUP)[at].view(torch.float8_e4m3fn).float()
-    e = torch.stack([codes & 15, codes >> 4], dim=-1).reshape(*at.shape, ROW // 8, 2, 4).transpose(-1, -2)
+    e = torch.stack([codes & 15, codes >> 4], dim=-1)
     v = _values(e.reshape(*at.shape, ROW // GROUP, GROUP)) * scales[..., None]
     return v.reshape(*at.shape, ROW)
 
