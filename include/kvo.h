@@ -431,6 +431,127 @@ int kvo_attend(kvo_handle* h, const int32_t* units, int32_t n_units, const void*
                void* stream);
 
 /* ------------------------------------------------------------------------
+ * Paged device cache (no passage of the pages; the library's own, for the
+ * layers whose cache stays on the device beside the offloaded ones: layers with
+ * a sliding window, draft heads, the chunk of a prefill pass).  Stateless, on
+ * caller buffers, asynchronous on `stream`, no allocation and no host read of
+ * device data: every call may be captured into a graph.
+ *
+ * The cache is a pool of n_blocks blocks of block_tokens rows (a multiple of 8)
+ * of 576 elements (latent 512, which is also the value | rope key 64), 16-byte
+ * aligned.  Row b * block_tokens + i of the pool ("slot") is row i of block b;
+ * token t of request r has slot block_table[r][t / block_tokens] *
+ * block_tokens + t mod block_tokens.  n_blocks * block_tokens < 2^31.
+ *   KVO_CACHE_BF16  a block is [block_tokens][576] bf16
+ *   KVO_CACHE_Q4    a block is [block_tokens][288] bytes of codes, then
+ *                   [block_tokens][36] bytes of scales: 36 groups of 16
+ *                   elements; an element's value is its E2M1 code (element 2b
+ *                   in the low four bits of byte b, 2b + 1 in the high ones)
+ *                   times its group's E4M3 scale (324 bytes a row, not 1152)
+ * kvo_paged_block_bytes: bytes of one block (0 on a bad argument).
+ * ------------------------------------------------------------------------ */
+#define KVO_CACHE_BF16 0
+#define KVO_CACHE_Q4 1
+int64_t kvo_paged_block_bytes(int32_t format, int32_t block_tokens);
+
+/*
+ * kvo_paged_plan: block tables and the slot map of a step, built on the device
+ * from the requests' lengths.  Request r caches lengths[r] tokens and gets
+ * new_tokens[r] more; new_tokens[r] < 0 ends it.
+ *   lengths, new_tokens : device int32 [n_requests] (n_requests <= 4096)
+ *   block_table : device int32 [n_requests][max_blocks] (in/out): the entries
+ *                 of the blocks that a request newly needs are written, in
+ *                 table order, the others left as they were
+ *   ring        : device int32 [ring_size] (in/out): ids of free blocks, those
+ *                 at positions ring_in[0] .. ring_in[1] - 1 modulo ring_size.
+ *                 Blocks are taken from the front in request order; blocks that
+ *                 are given up are put behind the end in request order, so they
+ *                 can be taken by the next call at the earliest.  ring_size at
+ *                 least the number of blocks.
+ *   ring_in, ring_out : device int64 [2], may be the same
+ *   window, sinks : window > 0: a growing request also gives up the blocks that
+ *                 no position from its new length on sees (every token of the
+ *                 block is at or below new length - window, and at or past
+ *                 block ceil(sinks / block_tokens)).  Their table entries stay
+ *                 and must not be read past the step's own positions.  The same
+ *                 window and sinks in every call of a request.  0: none.
+ *   lengths_out : device int32 [n_requests], may be lengths: the new length, 0
+ *                 for an ended request
+ *   kv_lens     : device int32 [n_requests]: the new length, 0 for a refused
+ *                 request (kvo_paged_attend then gives its tokens 0 and -inf)
+ *   cu_new      : device int32 [n_requests + 1]: new tokens before each request
+ *                 (refused ones count: they are the caller's layout)
+ *   slots       : device int32 [n_slots]: slot of every new token, requests in
+ *                 order; -1 for refused ones and behind the last
+ *   status      : device int32 [n_requests]: KVO_OK; KVO_ERANGE: the length is
+ *                 negative or passes max_blocks * block_tokens, or the tokens
+ *                 pass n_slots; KVO_ECAPACITY: the request needs blocks and
+ *                 those that requests 0..r need are more than the free ones.
+ *                 A refused request changes nothing.
+ * Lengths of the next call are this call's lengths_out.  An unlisted block id
+ * in the ring is not checked here (kvo_paged_write and _attend do).
+ * Errors: KVO_EINVAL, KVO_ECUDA.
+ */
+int kvo_paged_plan(const int32_t* lengths, const int32_t* new_tokens, int32_t n_requests,
+                   int32_t block_tokens, int32_t max_blocks, int32_t window, int32_t sinks,
+                   int32_t* block_table, int32_t* ring, int32_t ring_size, const int64_t* ring_in,
+                   int64_t* ring_out, int32_t* lengths_out, int32_t* kv_lens, int32_t* cu_new,
+                   int32_t* slots, int32_t n_slots, int32_t* status, void* stream);
+
+/*
+ * kvo_paged_write: row i of `rows` (device bf16 [n_rows][576], 16-byte aligned)
+ * into slot slots[i] (device int32 [n_rows]) of the pool; a slot below 0 or past
+ * the pool is skipped.  The slots of one call are distinct.  KVO_CACHE_Q4: a
+ * group's scale is its largest magnitude / 6 rounded to E4M3 (nearest even, at
+ * most 448), an element's code its quotient by that scale rounded to E2M1
+ * (nearest, ties to the even code, at most 6); a group with an element that is
+ * not finite reads back as NaN.
+ * kvo_paged_read: the values at slots[i] into row i of `rows` as bf16 (exact in
+ * both formats); rows whose slot is skipped are left as they were.
+ * Errors: KVO_EINVAL, KVO_ECUDA.
+ */
+int kvo_paged_write(const void* rows, const int32_t* slots, int64_t n_rows, void* pool,
+                    int64_t n_blocks, int32_t block_tokens, int32_t format, void* stream);
+int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,
+                   const int32_t* slots, int64_t n_rows, void* rows, void* stream);
+
+/*
+ * kvo_paged_attend: absorbed latent attention (the formula of kvo_attend) over
+ * the cached rows, causal, with an optional sliding window and sinks.  Query
+ * token i of request r (tokens cu_tokens[r] .. cu_tokens[r + 1] - 1, n_q of
+ * them) is at position p = kv_lens[r] - n_q + i and sees token t when t <= p
+ * and (window == 0 or t > p - window or t < sinks) and t's block is mapped.  A
+ * position that sees nothing gets 0 and -inf.
+ *   block_table : device int32 [n_requests][max_blocks]; an id below 0 or past
+ *                 the pool is not mapped.  Blocks that no position sees are
+ *                 never read.
+ *   kv_lens     : device int32 [n_requests] cached tokens, the queries' own included
+ *   cu_tokens   : device int32 [n_requests + 1], not decreasing, from 0 up to n_tokens
+ *   queries     : device bf16 [n_tokens][n_heads][576], 16-byte aligned; any n_heads <= 8192
+ *   out         : device bf16 [n_tokens][n_heads][512] (written), 16-byte aligned
+ *   lse         : device float [n_tokens][n_heads] (written), nullable
+ *                 rows from cu_tokens[n_requests] on are left as they were
+ *   workspace   : device scratch, 256-byte aligned, at least
+ *                 kvo_paged_attend_workspace_size() bytes (of the current
+ *                 device; 0 on a bad argument); no initialisation, not
+ *                 preserved; one per call in flight
+ *   status      : device uint32, nullable: set to 0, then nonzero if a bounded
+ *                 wait expired (the outputs are then not valid)
+ * Precision: scores and sums in fp32 on exact products; the softmax weights of
+ * the value product are rounded to bf16 (KVO_CACHE_Q4: fp16), their sum is not;
+ * out is rounded to bf16.  The same inputs give the same bits.
+ * Errors (nothing launched): KVO_EINVAL, KVO_ECUDA.
+ */
+size_t kvo_paged_attend_workspace_size(int32_t n_requests, int32_t n_tokens, int32_t n_heads,
+                                       int32_t device);
+int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,
+                     const int32_t* block_table, int32_t max_blocks, const int32_t* kv_lens,
+                     const int32_t* cu_tokens, int32_t n_requests, const void* queries,
+                     int32_t n_tokens, int32_t n_heads, float scale, int32_t window, int32_t sinks,
+                     void* out, float* lse, void* workspace, size_t workspace_bytes,
+                     uint32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------
  * Layerwise prefill offload ([LS] section 3 "Layerwise Prefill Offload":
  * "Buffer planning", "Execution pipeline", "Reuse invariant"; [FO] prefill
  * paragraph: four trays, tray B0 bound to the first layer, onload_layer_map).

@@ -1,0 +1,442 @@
+// Paged device cache: block tables and slot maps built on the GPU, rows written
+// into the cache (16 bits, or quantized to 4) and read back.  Layout of a block:
+// kvo_paged.cuh.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvo_paged.cuh"
+
+namespace kvo {
+
+using namespace paged;
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// First block that a position at or after length L can still see behind the
+// sinks' blocks: blocks [sb, dead_end(L)) are seen by none.
+__device__ __forceinline__ int dead_end(int L, int B, int window, int sb) {
+  if (window <= 0) return sb;
+  const int low = L - window + 1;  // lowest visible token of position L
+  return max(sb, low > 0 ? low / B : 0);
+}
+
+// ---------------------------------------------------------------------------
+// plan: one CTA.  Each request's needs (new blocks, new tokens, blocks given
+// back) are prefix-summed over the requests, then the flat lists of new blocks,
+// released blocks and slots are filled by all threads, each entry finding its
+// request by a search in the prefix arrays (shared memory).
+// Latency is all it costs (a few KB read and written): one launch, and about
+// as many barriers as there are prefix sums.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs a) {
+  extern __shared__ int32_t sm[];
+  __shared__ int64_t warp_sums[33];
+  const int R = a.R, B = a.B;
+  int32_t* cu = sm;              // [R + 1] new tokens before each request
+  int32_t* nb = cu + R + 1;      // [R + 1] new blocks before each request
+  int32_t* rel = nb + R + 1;     // [R + 1] released blocks before each request
+  int32_t* old = rel + R + 1;    // [R] cached tokens; -1: refused
+  const int sb = (a.sinks + B - 1) / B;
+  const int64_t head = a.ring_in[0], tail = a.ring_in[1];
+  const int64_t F = a.ring_size;
+  int64_t avail = tail - head;
+  avail = avail < 0 || head < 0 ? 0 : (avail > F ? F : avail);
+  int64_t tok0 = 0, blk0 = 0, rel0 = 0;
+  for (int base = 0; base < R; base += kPlanThreads) {
+    const int r = base + (int)threadIdx.x;
+    int len = 0, n = 0, have = 0;
+    int64_t grow = 0, need = 0;
+    bool fits = true;
+    if (r < R) {
+      len = a.lengths[r];
+      n = a.new_tokens[r];
+      grow = n > 0 ? n : 0;
+      fits = len >= 0 && (int64_t)len + grow <= (int64_t)a.M * B;
+    }
+    int64_t total;
+    const int64_t c = tok0 + block_exclusive_sum<kPlanThreads>(grow, warp_sums, &total);
+    tok0 += total;
+    if (r < R) {
+      cu[r] = (int32_t)(c < INT32_MAX ? c : INT32_MAX);
+      if (grow > 0 && c + grow > a.n_slots) fits = false;
+      have = fits ? (len + B - 1) / B : 0;
+      need = fits ? (len + grow + B - 1) / B - have : 0;
+    }
+    const int64_t nb_at = block_exclusive_sum<kPlanThreads>(need, warp_sums, &total);
+    const bool served = fits && (need == 0 || blk0 + nb_at + need <= avail);
+    // blocks are taken in request order: the served requests that need some are
+    // a prefix of those, so what comes before a served one is served too
+    int64_t gone = 0;
+    if (r < R) {
+      nb[r] = (int32_t)(blk0 + nb_at < avail ? blk0 + nb_at : avail);
+      if (served && n < 0) {
+        gone = min(sb, have) + max(0, have - dead_end(len, B, a.window, sb));
+      } else if (served) {
+        const int hi = min(dead_end(len + (int)grow, B, a.window, sb), have + (int)need);
+        gone = max(0, hi - dead_end(len, B, a.window, sb));
+      }
+    }
+    blk0 += total;
+    const int64_t rel_at = rel0 + block_exclusive_sum<kPlanThreads>(gone, warp_sums, &total);
+    rel0 += total;
+    if (r < R) {
+      rel[r] = (int32_t)(rel_at < F ? rel_at : F);
+      const int after = n < 0 ? 0 : len + (int)grow;
+      old[r] = served ? len : -1;
+      a.lengths_out[r] = served ? after : len;
+      a.kv_lens[r] = served ? after : 0;
+      a.status[r] = served ? KVO_OK : (fits ? KVO_ECAPACITY : KVO_ERANGE);
+    }
+    // the next chunk's served requests start behind what this one took
+    if (blk0 > avail) blk0 = avail + 1;
+  }
+  __syncthreads();
+  // new blocks taken: the last served request's end
+  if (threadIdx.x == 0) {
+    cu[R] = (int32_t)(tok0 < INT32_MAX ? tok0 : INT32_MAX);
+    rel[R] = (int32_t)(rel0 < F ? rel0 : F);
+  }
+  __syncthreads();
+  for (int r = threadIdx.x; r <= R; r += kPlanThreads) a.cu_new[r] = cu[r];
+  __shared__ int32_t taken;
+  if (threadIdx.x == 0) taken = 0;
+  __syncthreads();
+  for (int r = threadIdx.x; r < R; r += kPlanThreads) {
+    if (old[r] >= 0) {
+      const int grow = cu[r + 1] - cu[r];
+      const int need = (old[r] + grow + B - 1) / B - (old[r] + B - 1) / B;
+      if (need > 0) atomicMax(&taken, nb[r] + need);
+    }
+  }
+  __syncthreads();
+  const int n_new = taken, n_rel = rel[R];
+  for (int i = threadIdx.x; i < n_new; i += kPlanThreads) {
+    // the last request that starts at or before entry i and needs blocks
+    const int r = segment_of(nb, R, i);
+    a.table[(int64_t)r * a.M + (old[r] + B - 1) / B + (i - nb[r])] = a.ring[(head + i) % F];
+  }
+  __syncthreads();  // tables complete; every taken entry read before the ring is written
+  for (int i = threadIdx.x; i < n_rel; i += kPlanThreads) {
+    const int r = segment_of(rel, R, i);
+    const int k = i - rel[r], len = old[r];
+    int j;
+    if (a.new_tokens[r] < 0) {
+      const int s = min(sb, (len + B - 1) / B);
+      j = k < s ? k : dead_end(len, B, a.window, sb) + (k - s);
+    } else {
+      j = dead_end(len, B, a.window, sb) + k;
+    }
+    a.ring[(tail + i) % F] = a.table[(int64_t)r * a.M + j];
+  }
+  for (int i = threadIdx.x; i < a.n_slots; i += kPlanThreads) {
+    int32_t slot = -1;
+    if (i < cu[R]) {
+      const int r = segment_of(cu, R, i);
+      if (old[r] >= 0) {
+        const int t = old[r] + (i - cu[r]);
+        slot = a.table[(int64_t)r * a.M + t / B] * B + t % B;
+      }
+    }
+    a.slots[i] = slot;
+  }
+  if (threadIdx.x == 0) {
+    a.ring_out[0] = head + n_new;
+    a.ring_out[1] = tail + n_rel;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows.  A thread handles one group of 16 elements (32 bytes of a bf16 row);
+// a CTA eight rows.
+// ---------------------------------------------------------------------------
+constexpr int kRowsPerCta = 8;
+constexpr int kRowThreads = kRowsPerCta * kGroups;
+
+__device__ __forceinline__ uint8_t* q4_codes(uint8_t* pool, int64_t slot, int B) {
+  return pool + (slot / B) * ((int64_t)B * kRowBytesQ4) + (slot % B) * kCodeBytes;
+}
+__device__ __forceinline__ uint8_t* q4_scales(uint8_t* pool, int64_t slot, int B) {
+  return pool + (slot / B) * ((int64_t)B * kRowBytesQ4) + (int64_t)B * kCodeBytes + (slot % B) * kGroups;
+}
+
+// E2M1 code of a >= 0 (already divided by the scale): round to nearest, a tie
+// to the even code, above 5 to the largest value.
+__device__ __forceinline__ uint32_t e2m1_of(float a) {
+  return (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) + (uint32_t)(a >= 1.75f) +
+         (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.f);
+}
+
+template <bool kQ4>
+__global__ void __launch_bounds__(kRowThreads) write_paged_kernel(PagedRowsArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x / kGroups;
+  const int g = threadIdx.x % kGroups;
+  if (i >= a.n) return;
+  const int64_t slot = __ldg(a.slots + i);
+  if (slot < 0 || slot >= a.pool_rows) return;
+  const uint4* src = reinterpret_cast<const uint4*>(a.rows + i * kRow + g * kGroup);
+  const uint4 x0 = __ldg(src), x1 = __ldg(src + 1);
+  if (!kQ4) {
+    uint4* dst = reinterpret_cast<uint4*>(a.pool + slot * kRowBytes16 + g * kGroup * 2);
+    dst[0] = x0;
+    dst[1] = x1;
+    return;
+  }
+  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+  // the largest magnitude, by its bits: NaN above infinity above every finite value
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+  uint2 codes = make_uint2(0u, 0u);
+  uint8_t sbits = 0x7f;  // a group that is not finite reads as NaN
+  if (top < 0x7f80u) {
+    const float amax = __uint_as_float(top << 16);
+    sbits = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.f), __NV_SATFINITE, __NV_E4M3);
+    const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(sbits, __NV_E4M3)));
+    if (s > 0.f) {
+      uint32_t c[2] = {0u, 0u};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t lo = e2m1_of(__fdiv_rn(fabsf(bf_lo(w[k])), s)) | ((w[k] >> 12) & 8u);
+        const uint32_t hi = e2m1_of(__fdiv_rn(fabsf(bf_hi(w[k])), s)) | ((w[k] >> 28) & 8u);
+        c[k >> 2] |= (lo | (hi << 4)) << (8 * (k & 3));
+      }
+      codes = make_uint2(c[0], c[1]);
+    }
+  }
+  *reinterpret_cast<uint2*>(q4_codes(a.pool, slot, a.B) + g * (kGroup / 2)) = codes;
+  q4_scales(a.pool, slot, a.B)[g] = sbits;
+}
+
+template <bool kQ4>
+__global__ void __launch_bounds__(kRowThreads) read_paged_kernel(PagedRowsArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x / kGroups;
+  const int g = threadIdx.x % kGroups;
+  if (i >= a.n) return;
+  const int64_t slot = __ldg(a.slots + i);
+  if (slot < 0 || slot >= a.pool_rows) return;
+  uint4* dst = reinterpret_cast<uint4*>(a.rows + i * kRow + g * kGroup);
+  if (!kQ4) {
+    const uint4* src = reinterpret_cast<const uint4*>(a.pool + slot * kRowBytes16 + g * kGroup * 2);
+    const uint4 x0 = src[0], x1 = src[1];
+    dst[0] = x0;
+    dst[1] = x1;
+    return;
+  }
+  const uint2 codes = *reinterpret_cast<const uint2*>(q4_codes(a.pool, slot, a.B) + g * (kGroup / 2));
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(q4_scales(a.pool, slot, a.B)[g], __NV_E4M3)));
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t b = ((k < 4 ? codes.x : codes.y) >> (8 * (k & 3))) & 0xffu;
+    // a code's magnitude: exponent field 0 is a multiple of 1/2, else 2^(e - 1) (1 + m / 2)
+    float v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t c = (b >> (4 * h)) & 15u, e = (c >> 1) & 3u, m = c & 1u;
+      const float x = e == 0u ? 0.5f * (float)m : (float)(2u + m) * 0.25f * (float)(1u << e);
+      v[h] = (c & 8u) ? -x : x;
+    }
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[0] * s, v[1] * s);  // exact
+    w[k] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <typename K>
+cudaError_t launch_rows(K kernel, const PagedRowsArgs& a, cudaStream_t s) {
+  if (a.n <= 0) return cudaSuccess;
+  const int64_t grid = (a.n + kRowsPerCta - 1) / kRowsPerCta;
+  kernel<<<(unsigned)grid, kRowThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+int fail(int code, const char* msg) { return set_error(code, msg); }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The cache's shape: KVO_OK, or the error that the calls below share.
+int check_cache(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format) {
+  if (!pool) return fail(KVO_EINVAL, "pool is NULL");
+  if (!aligned(pool, 16)) return fail(KVO_EINVAL, "pool not 16-byte aligned");
+  if (format != KVO_CACHE_BF16 && format != KVO_CACHE_Q4) return fail(KVO_EINVAL, "unknown cache format");
+  if (block_tokens < 8 || block_tokens > 65536 || block_tokens % 8 != 0)
+    return fail(KVO_EINVAL, "block_tokens must be a multiple of 8 in 8 .. 65536");
+  if (n_blocks < 1 || n_blocks > ((int64_t)1 << 31) / block_tokens - 1)
+    return fail(KVO_EINVAL, "n_blocks * block_tokens must be positive and below 2^31");
+  return KVO_OK;
+}
+
+int rows_call(PagedRowsArgs& a, const void* rows, const int32_t* slots, int64_t n_rows, const void* pool,
+              int64_t n_blocks, int32_t block_tokens, int32_t format) {
+  const int rc = check_cache(pool, n_blocks, block_tokens, format);
+  if (rc != KVO_OK) return rc;
+  if (n_rows < 0 || n_rows >= (int64_t)1 << 31) return fail(KVO_EINVAL, "n_rows out of range");
+  if (n_rows > 0 && (!rows || !slots)) return fail(KVO_EINVAL, "NULL argument");
+  if (!aligned(rows, 16) || !aligned(slots, 4)) return fail(KVO_EINVAL, "rows not 16-byte or slots not 4-byte aligned");
+  a.pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+  a.pool_rows = n_blocks * block_tokens;
+  a.B = block_tokens;
+  a.slots = slots;
+  a.n = n_rows;
+  a.rows = static_cast<uint16_t*>(const_cast<void*>(rows));
+  return KVO_OK;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s) {
+  const size_t smem = (4 * (size_t)a.R + 3) * 4;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(plan_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  plan_paged_kernel<<<1, kPlanThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+cudaError_t launch_paged_write(const PagedRowsArgs& a, bool q4, cudaStream_t s) {
+  return q4 ? launch_rows(write_paged_kernel<true>, a, s) : launch_rows(write_paged_kernel<false>, a, s);
+}
+cudaError_t launch_paged_read(const PagedRowsArgs& a, bool q4, cudaStream_t s) {
+  return q4 ? launch_rows(read_paged_kernel<true>, a, s) : launch_rows(read_paged_kernel<false>, a, s);
+}
+
+}  // namespace kvo
+
+extern "C" {
+
+int64_t kvo_paged_block_bytes(int32_t format, int32_t block_tokens) {
+  if (block_tokens < 8 || block_tokens > 65536 || block_tokens % 8 != 0) return 0;
+  if (format == KVO_CACHE_BF16) return (int64_t)block_tokens * kvo::paged::kRowBytes16;
+  if (format == KVO_CACHE_Q4) return (int64_t)block_tokens * kvo::paged::kRowBytesQ4;
+  return 0;
+}
+
+int kvo_paged_plan(const int32_t* lengths, const int32_t* new_tokens, int32_t n_requests, int32_t block_tokens,
+                   int32_t max_blocks, int32_t window, int32_t sinks, int32_t* block_table, int32_t* ring,
+                   int32_t ring_size, const int64_t* ring_in, int64_t* ring_out, int32_t* lengths_out,
+                   int32_t* kv_lens, int32_t* cu_new, int32_t* slots, int32_t n_slots, int32_t* status, void* stream) {
+  using namespace kvo;
+  if (!lengths || !new_tokens || !block_table || !ring || !ring_in || !ring_out || !lengths_out || !kv_lens ||
+      !cu_new || !status || (!slots && n_slots != 0))
+    return fail(KVO_EINVAL, "NULL argument");
+  if (!aligned(lengths, 4) || !aligned(new_tokens, 4) || !aligned(block_table, 4) || !aligned(ring, 4) ||
+      !aligned(ring_in, 8) || !aligned(ring_out, 8) || !aligned(lengths_out, 4) || !aligned(kv_lens, 4) ||
+      !aligned(cu_new, 4) || !aligned(slots, 4) || !aligned(status, 4))
+    return fail(KVO_EINVAL, "array not aligned to its elements");
+  if (n_requests < 1 || n_requests > paged::kMaxRequests) return fail(KVO_EINVAL, "n_requests must be in 1 .. 4096");
+  if (block_tokens < 8 || block_tokens > 65536 || block_tokens % 8 != 0)
+    return fail(KVO_EINVAL, "block_tokens must be a multiple of 8 in 8 .. 65536");
+  if (max_blocks < 1 || (int64_t)max_blocks * block_tokens > paged::kMaxTokens)
+    return fail(KVO_EINVAL, "max_blocks * block_tokens must be in 1 .. 2^30");
+  if (ring_size < 1 || n_slots < 0 || window < 0 || sinks < 0)
+    return fail(KVO_EINVAL, "ring_size, n_slots, window or sinks out of range");
+  PagedPlanArgs a{};
+  a.lengths = lengths;
+  a.new_tokens = new_tokens;
+  a.R = n_requests;
+  a.B = block_tokens;
+  a.M = max_blocks;
+  // beyond every token that a table reaches, they say no more
+  a.window = (int32_t)(window < paged::kMaxTokens ? window : paged::kMaxTokens);
+  a.sinks = (int32_t)(sinks < paged::kMaxTokens ? sinks : paged::kMaxTokens);
+  a.table = block_table;
+  a.ring = ring;
+  a.ring_size = ring_size;
+  a.ring_in = ring_in;
+  a.ring_out = ring_out;
+  a.lengths_out = lengths_out;
+  a.kv_lens = kv_lens;
+  a.cu_new = cu_new;
+  a.slots = slots;
+  a.n_slots = n_slots;
+  a.status = status;
+  const cudaError_t e = launch_paged_plan(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return set_cuda_error(e, "paged plan launch");
+  return KVO_OK;
+}
+
+int kvo_paged_write(const void* rows, const int32_t* slots, int64_t n_rows, void* pool, int64_t n_blocks,
+                    int32_t block_tokens, int32_t format, void* stream) {
+  kvo::PagedRowsArgs a{};
+  const int rc = kvo::rows_call(a, rows, slots, n_rows, pool, n_blocks, block_tokens, format);
+  if (rc != KVO_OK) return rc;
+  const cudaError_t e = kvo::launch_paged_write(a, format == KVO_CACHE_Q4, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return kvo::set_cuda_error(e, "paged write launch");
+  return KVO_OK;
+}
+
+int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format, const int32_t* slots,
+                   int64_t n_rows, void* rows, void* stream) {
+  kvo::PagedRowsArgs a{};
+  const int rc = kvo::rows_call(a, rows, slots, n_rows, pool, n_blocks, block_tokens, format);
+  if (rc != KVO_OK) return rc;
+  const cudaError_t e = kvo::launch_paged_read(a, format == KVO_CACHE_Q4, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return kvo::set_cuda_error(e, "paged read launch");
+  return KVO_OK;
+}
+
+size_t kvo_paged_attend_workspace_size(int32_t n_requests, int32_t n_tokens, int32_t n_heads, int32_t device) {
+  if (n_requests < 1 || n_requests > kvo::paged::kMaxRequests || n_tokens < 0 || n_heads < 1 || n_heads > 8192) return 0;
+  int n_sm = 0;
+  if (cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
+  return kvo::paged_attend_workspace(n_requests, n_tokens, n_heads, n_sm);
+}
+
+int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,
+                     const int32_t* block_table, int32_t max_blocks, const int32_t* kv_lens, const int32_t* cu_tokens,
+                     int32_t n_requests, const void* queries, int32_t n_tokens, int32_t n_heads, float scale,
+                     int32_t window, int32_t sinks, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                     uint32_t* status, void* stream) {
+  using namespace kvo;
+  const int rc = check_cache(pool, n_blocks, block_tokens, format);
+  if (rc != KVO_OK) return rc;
+  if (!block_table || !kv_lens || !cu_tokens || !workspace) return fail(KVO_EINVAL, "NULL argument");
+  if (n_requests < 1 || n_requests > paged::kMaxRequests) return fail(KVO_EINVAL, "n_requests must be in 1 .. 4096");
+  if (max_blocks < 1 || (int64_t)max_blocks * block_tokens > paged::kMaxTokens)
+    return fail(KVO_EINVAL, "max_blocks * block_tokens must be in 1 .. 2^30");
+  if (n_heads < 1 || n_heads > 8192) return fail(KVO_EINVAL, "n_heads must be in 1 .. 8192");
+  if (n_tokens < 0 || (int64_t)n_tokens * n_heads >= (int64_t)1 << 30)
+    return fail(KVO_EINVAL, "n_tokens * n_heads must be below 2^30");
+  if (n_tokens > 0 && (!queries || !out)) return fail(KVO_EINVAL, "NULL argument");
+  if (!aligned(queries, 16) || !aligned(out, 16)) return fail(KVO_EINVAL, "queries or out not 16-byte aligned");
+  if (!aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(cu_tokens, 4) || !aligned(lse, 4) || !aligned(status, 4))
+    return fail(KVO_EINVAL, "array not aligned to its elements");
+  if (!aligned(workspace, 256)) return fail(KVO_EINVAL, "workspace not 256-byte aligned");
+  if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return fail(KVO_EINVAL, "scale is not finite");
+  if (window < 0 || sinks < 0) return fail(KVO_EINVAL, "window and sinks must not be negative");
+  int dev = 0, n_sm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return fail(KVO_ECUDA, "no current device");
+  if (workspace_bytes < paged_attend_workspace(n_requests, n_tokens, n_heads, n_sm))
+    return fail(KVO_EINVAL, "workspace too small");
+  PagedAttendArgs a{};
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.n_blocks = n_blocks;
+  a.B = block_tokens;
+  a.M = max_blocks;
+  a.R = n_requests;
+  a.table = block_table;
+  a.kv_lens = kv_lens;
+  a.cu = cu_tokens;
+  a.q = static_cast<const uint16_t*>(queries);
+  a.n_tokens = n_tokens;
+  a.H = n_heads;
+  a.window = (int32_t)(window < paged::kMaxTokens ? window : paged::kMaxTokens);
+  a.sinks = (int32_t)(sinks < paged::kMaxTokens ? sinks : paged::kMaxTokens);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.status = status;
+  a.wait_ns = 2000000000ull;
+  a.workers = n_sm;
+  paged_attend_carve(a, static_cast<uint8_t*>(workspace));
+  const cudaError_t e = launch_paged_attend(a, format == KVO_CACHE_Q4, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return set_cuda_error(e, "paged attention launch");
+  return KVO_OK;
+}
+
+}  // extern "C"

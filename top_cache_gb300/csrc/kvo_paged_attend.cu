@@ -1,0 +1,1074 @@
+// Attention over the paged device cache, in 16 or 4 bits, with a sliding window
+// and sinks, on the 5th-generation tensor cores.
+//
+// Absorbed latent attention (as kvo_attend): a cached row is 576 elements,
+// latent 512 (also the value) | rope key 64.  Query token i of request r is at
+// position p = kv_len - n_q + i and sees token t when t <= p and (no window, or
+// t > p - window, or t < sinks) and its block is mapped; for each head
+//   s_t = scale * q . row_t,  out = sum_t softmax(s)_t row_t[0:512],
+//   lse = log sum_t exp(s_t);  nothing visible: out 0, lse -inf.
+//
+// Shape of the work.  The rows of a request's queries, (token, head) in memory
+// order, are cut into tiles of N = 16, 32 or 64; a tile walks the 128-token
+// blocks that any of its positions sees.  Keys and queries change places in the
+// MMAs: S^T = K Q^T has M = 128 tokens and N = the tile's rows, O^T = V^T P^T
+// has M = 128 of the 512 value elements.  So a tile of 16 rows costs 16 columns
+// (heads on the M side would be padded to 128), and O^T of 64 rows, 4 x 64 fp32
+// columns, leaves TMEM room for S^T without splitting the value elements over
+// CTAs.  A tcgen05.mma with both operands in shared memory takes the time of
+// reading them at 128 bytes a clock: 32 + N / 4 clocks for M = 128, K = 16, when
+// the issuing warp runs uniformly (39, 40 and 48 measured at N = 16, 32, 64; 69
+// whatever N from inside a one-thread branch).  N = 64 therefore peaks at 2/3
+// of the tensor rate.
+//
+// One persistent CTA per SM, warp-specialised:
+//   producers    the tile's queries, then each block's rows into a ring of
+//                pairs of 128-byte-swizzled K-major slabs (128 tokens x 64
+//                elements); the same bytes are the K-major A of S^T and the
+//                MN-major A of O^T.  16 bits: 4 warps, 16-byte cp.async (a row
+//                not to be read is zero-filled).  4 bits: 8 warps hold the next
+//                block's codes in registers while they expand this one's to
+//                fp16 (exact; queries are scaled by a power of two per row to
+//                fit fp16, undone in the scores)
+//   softmax      8 warps, one token (TMEM lane) per thread and half of the
+//                tile's rows.  Per-thread sums; a running maximum that moves
+//                only when a score passes it by 2^8, so most blocks need no
+//                reduction over the tokens, only a vote
+//   MMA          one warp
+// Every wait is bounded; when one expires the error word is set and the roles
+// stop.
+//
+// Split.  A schedule kernel lists the tiles with their blocks.  Few tiles (at
+// most kListTiles): the list's blocks are cut evenly over the CTAs, whatever
+// tiles they cross, so one long request fills the GPU; a tile that no CTA has
+// alone leaves partial (O, m, l) in the workspace, at most two per CTA, and a
+// third kernel joins them in CTA order.  Many tiles: CTA c takes tiles c, c +
+// CTAs, ... whole (neighbours cost alike).  Results do not depend on timing.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvo_paged.cuh"
+
+namespace kvo {
+
+using namespace paged;
+
+namespace {
+
+constexpr int kBlk = 128;            // tokens per block of the walk: M of S^T, K of O^T
+constexpr int kSlabs = kRow / 64;    // 9: eight of the value, then rope
+constexpr int kListTiles = 2048;     // most tiles that are listed and split
+constexpr int kTileCost = 1;         // a tile's own cost, in blocks (queries in, output out)
+constexpr int kMinShare = 2;         // least units a CTA is given when the list is split
+constexpr int kSoftWarps = 8;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr uint32_t kSlab = kBlk * 128;       // bytes of one slab of a block
+constexpr uint32_t kPair = 2 * kSlab;
+constexpr int kMaxRing = 5;
+constexpr float kNone = -3.0e38f;            // running maximum before any visible token
+constexpr float kRescale = 8.f;              // log2: how far a score may pass the running maximum
+
+template <int N, bool kQ4>
+struct Shape {
+  static constexpr int kProducers = kQ4 ? 256 : 128;
+  static constexpr int kThreads = kProducers + kSoftThreads + 32;
+  static constexpr int kNC = N / 2;                    // rows of one softmax thread
+  static constexpr bool kSharedP = N == 64;            // P^T lies in the rope slab's place
+  static constexpr int kRing = N == 64 ? 4 : kMaxRing; // pairs
+  static constexpr uint32_t kQSlab = N * 128;
+  static constexpr uint32_t kQOff = 0;
+  static constexpr uint32_t kRingOff = kSlabs * kQSlab;
+  static constexpr uint32_t kRopeOff = kRingOff + kRing * kPair;
+  static constexpr uint32_t kPOff = kSharedP ? kRopeOff : kRopeOff + kSlab;
+  static constexpr uint32_t kPBytes = kSharedP ? 0u : N * 256u;
+  static constexpr uint32_t kMiscOff = kRopeOff + kSlab + kPBytes;
+  // misc: running maxima, row positions and query factors [2][N], warp maxima and sums [8][NC], 1 / l [N]
+  static constexpr uint32_t kMiscBytes = (3 * 2 * N + 2 * 8 * kNC + N) * 4;
+  static constexpr uint32_t kBarOff = kMiscOff + kMiscBytes;
+  static constexpr uint32_t kSmem = kBarOff + 256 + 1024;  // barriers and flags, alignment slack
+  static constexpr uint32_t kTmem = N == 64 ? 512 : N == 32 ? 256 : 128;
+  static constexpr uint32_t kColS = 4 * N;             // O^T: value elements 128 i.. at columns i * N
+  static constexpr float kBias = kQ4 ? 7.f : 0.f;      // P is 2^kBias exp2(..): keeps small weights out of fp16's subnormals
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+  static_assert(kRingOff % 1024 == 0 && kPOff % 1024 == 0 && kBarOff % 8 == 0, "swizzled tiles sit on 1 KB boundaries");
+};
+
+// ---- tcgen05 ------------------------------------------------------------------------------
+// Shared-memory matrix descriptor, 128-byte swizzle (byte offsets in 16-byte units).
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor of kind::f16: A and B both bf16 or both f16, fp32 D.
+constexpr uint32_t idesc(bool bf16, int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+         ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Issued by the lane whose `el` is set; the warp runs it uniformly.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(el)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(el)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t el;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el));
+  return el;
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 8 consecutive 32-bit columns of this thread's TMEM lane (kNC in steps of 8).
+__device__ __forceinline__ void tmem_ld8(uint32_t t, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t)
+               : "memory");
+#pragma unroll
+  for (int c = 0; c < 8; ++c) v[c] = __uint_as_float(r[c]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t t, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
+}
+template <int NC>
+__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[NC]) {
+#pragma unroll
+  for (int c = 0; c < NC; c += 8) tmem_ld8(t + (uint32_t)c, v + c);
+}
+
+// ---- shared memory -------------------------------------------------------------------------
+// 16-byte chunk c (0..7) of row r in a 128-byte-swizzled slab (1 KB aligned).
+__device__ __forceinline__ uint32_t swz(uint32_t slab, int r, int c) {
+  return slab + (uint32_t)r * 128u + ((uint32_t)(c ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// One arrival once every cp.async that this thread has issued so far has landed.
+__device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void st_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_u16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+// Whether any of the first `threads` threads at barrier `id` has p set.
+__device__ __forceinline__ bool named_any(uint32_t id, uint32_t threads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+// 2^x, hardware approximation (relative error near 2^-22); 2^-inf = 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- the work -------------------------------------------------------------------------------
+// One tile, or the part of its blocks that this CTA has.
+struct Seg {
+  int r;                 // request
+  int64_t grow;          // first row of the tile among all (token, head) rows
+  int row0, nrows;       // first row within the request, rows
+  int pos0, H;           // position of the request's first query token, heads
+  int pmin, pmax;        // positions of the tile's first and last row
+  int lo, snk;           // window part starts here; tokens below snk are seen by all positions at or past them
+  int wlo, nsb, nblk;    // first block of the window part, blocks of the sinks before it, blocks
+  int b0, b1;            // this CTA's blocks of the list
+  int part;              // -1: whole tile, else its partial slot
+  __device__ __forceinline__ int block(int b) const { return b < nsb ? b : wlo + (b - nsb); }
+  __device__ __forceinline__ bool any_sees(int t) const { return t <= pmax && (t >= lo || t < snk); }
+};
+
+__device__ __forceinline__ void tile_of(const PagedAttendArgs& a, int N, int r, int row0, Seg& s) {
+  const int c0 = min(max(a.cu[r], 0), a.n_tokens), c1 = min(max(a.cu[r + 1], c0), a.n_tokens);
+  const int nq = c1 - c0;
+  const int kv = (int)min((int64_t)max(a.kv_lens[r], 0), (int64_t)a.M * a.B);
+  s.r = r;
+  s.H = a.H;
+  s.row0 = row0;
+  s.nrows = min(N, nq * a.H - row0);
+  s.grow = (int64_t)c0 * a.H + row0;
+  s.pos0 = kv - nq;
+  s.pmin = s.pos0 + row0 / a.H;
+  s.pmax = s.pos0 + (row0 + s.nrows - 1) / a.H;
+  s.lo = a.window > 0 ? max(0, s.pmin - a.window + 1) : 0;
+  s.snk = a.sinks;
+  s.wlo = 0;
+  s.nsb = 0;
+  s.nblk = 0;
+  if (s.pmax >= 0) {
+    const int nsb = (min(a.sinks, s.pmax + 1) + kBlk - 1) / kBlk;
+    const int wlo = s.lo / kBlk;
+    if (nsb < wlo) {
+      s.nsb = nsb;
+      s.wlo = wlo;
+    }
+    s.nblk = s.nsb + s.pmax / kBlk - s.wlo + 1;
+  }
+}
+__device__ __forceinline__ int request_rows(const PagedAttendArgs& a, int r) {
+  const int c0 = min(max(a.cu[r], 0), a.n_tokens), c1 = min(max(a.cu[r + 1], c0), a.n_tokens);
+  return (c1 - c0) * a.H;
+}
+
+// Parts of the workspace header.
+constexpr int kHdListed = 0, kHdTiles = 1, kHdWorkers = 2;
+
+// The segments of one CTA, in order; every warp that walks them calls next()
+// with all lanes.
+template <int N>
+struct Walk {
+  bool listed;
+  int tile, unit, end_tile, end_unit, n_tiles;
+  __device__ __forceinline__ void begin(const PagedAttendArgs& a) {
+    listed = a.head[kHdListed] != 0;
+    n_tiles = a.head[kHdTiles];
+    tile = (int)blockIdx.x;
+    unit = 0;
+    end_tile = n_tiles;
+    end_unit = 0;
+    if (listed) {
+      const int used = a.head[kHdWorkers], w = min((int)blockIdx.x, used);
+      const int2 s = a.start[w], e = a.start[min(w + 1, used)];
+      tile = s.x;
+      unit = s.y;
+      end_tile = e.x;
+      end_unit = e.y;
+    }
+  }
+  __device__ __forceinline__ bool next(const PagedAttendArgs& a, Seg& s) {
+    if (!listed) {
+      if (tile >= n_tiles) return false;
+      // request of the tile: 32-way search in tile_off
+      const int lane = threadIdx.x & 31;
+      int lo = 0, hi = a.R;
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, i = min(lo + (lane + 1) * step, hi);
+        const int below = __popc(__ballot_sync(kFull, i < hi && a.tile_off[i] <= tile));
+        hi = min(lo + (below + 1) * step, hi);
+        lo = lo + below * step;
+      }
+      tile_of(a, N, lo, (tile - a.tile_off[lo]) * N, s);
+      s.b0 = 0;
+      s.b1 = s.nblk;
+      s.part = -1;
+      tile += (int)gridDim.x;
+      return true;
+    }
+    while (tile < end_tile || (tile == end_tile && unit < end_unit)) {
+      const int4 d = a.tiles[tile];
+      tile_of(a, N, d.x, d.y, s);
+      const int last = tile == end_tile ? end_unit : s.nblk + kTileCost;
+      s.b0 = max(unit - kTileCost, 0);
+      s.b1 = max(last - kTileCost, 0);
+      const bool first = unit < kTileCost;  // has the tile's own unit
+      s.part = s.b0 == 0 && s.b1 == s.nblk ? -1 : (first ? 1 : 0);
+      ++tile;
+      unit = 0;
+      if (s.b0 < s.b1 || (s.nblk == 0 && first)) return true;
+    }
+    return false;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// schedule: one CTA.  Tiles per request; if they are few, the list of tiles,
+// the blocks before each, and where each CTA's even share starts.
+// ---------------------------------------------------------------------------
+constexpr int kSchedThreads = 1024;
+
+__global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAttendArgs a, int N) {
+  __shared__ int64_t warp_sums[33];
+  __shared__ int32_t off[kMaxRequests + 1];
+  int64_t total = 0, sum;
+  for (int base = 0; base < a.R; base += kSchedThreads) {
+    const int r = base + (int)threadIdx.x;
+    const int64_t n = r < a.R ? (request_rows(a, r) + N - 1) / N : 0;
+    const int64_t at = total + block_exclusive_sum<kSchedThreads>(n, warp_sums, &sum);
+    if (r < a.R) a.tile_off[r] = off[r] = (int32_t)at;
+    total += sum;
+  }
+  const int n_tiles = (int)total;
+  const bool listed = n_tiles <= kListTiles;
+  if (threadIdx.x == 0) {
+    a.tile_off[a.R] = n_tiles;
+    a.head[kHdListed] = listed ? 1 : 0;
+    a.head[kHdTiles] = n_tiles;
+    *a.status = 0u;
+  }
+  __syncthreads();
+  if (!listed) return;
+  // thread i lists tiles 2 i and 2 i + 1
+  int cost[2] = {0, 0};
+  int4 d[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = 2 * (int)threadIdx.x + k;
+    if (i < n_tiles) {
+      const int r = segment_of(off, a.R, i);
+      Seg s;
+      tile_of(a, N, r, (i - off[r]) * N, s);
+      cost[k] = s.nblk + kTileCost;
+      d[k] = make_int4(r, s.row0, s.nblk, 0);
+    }
+  }
+  int64_t units;
+  int64_t at = block_exclusive_sum<kSchedThreads>((int64_t)cost[0] + cost[1], warp_sums, &units);
+  const int64_t share = max((int64_t)kMinShare, (units + a.workers - 1) / a.workers);
+  const int used = (int)min((int64_t)a.workers, (units + share - 1) / share);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = 2 * (int)threadIdx.x + k;
+    if (i < n_tiles) {
+      d[k].w = (int)min(at, (int64_t)INT32_MAX);
+      a.tiles[i] = d[k];
+      // CTA w starts at unit w * units / used
+      for (int64_t w = (at * used + units - 1) / units; w < used; ++w) {
+        const int64_t u = w * units / used;
+        if (u >= at + cost[k]) break;
+        if (u >= at) a.start[w] = make_int2(i, (int)(u - at));
+      }
+      at += cost[k];
+    }
+  }
+  if (threadIdx.x == 0) {
+    a.start[used] = make_int2(n_tiles, 0);
+    a.head[kHdWorkers] = used;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// attention
+// ---------------------------------------------------------------------------
+struct Bars {
+  uint64_t q_full, q_free, r_full, r_free, s_full, p_full, o_done, o_free, fin;
+  uint64_t e_full[kMaxRing], e_free[kMaxRing];
+  uint32_t tmem, abort;
+};
+static_assert(sizeof(Bars) <= 256, "barriers");
+
+// 16 elements of E2M1 codes (8 bytes) times their scale: 32 bytes of fp16, exact.
+__device__ __forceinline__ void expand16(uint32_t c0, uint32_t c1, uint32_t s2, uint4& lo, uint4& hi) {
+  uint32_t r[8];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(c0));
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(c1));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r[k]) : "r"(r[k]), "r"(s2));
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+// Two E4M3 scales (low 16 bits) -> each one twice, as fp16 pairs.
+__device__ __forceinline__ void scales2(uint32_t b, uint32_t& s0, uint32_t& s1) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(b));
+  s0 = __byte_perm(h, h, 0x1010);
+  s1 = __byte_perm(h, h, 0x3232);
+}
+
+// Token t's row of the pool (-1: its block is not mapped).
+__device__ __forceinline__ int64_t pool_row(const PagedAttendArgs& a, const int32_t* table, int t) {
+  const int j = t / a.B;
+  const int32_t b = __ldg(table + j);
+  return b < 0 || (int64_t)b >= a.n_blocks ? -1 : (int64_t)b * a.B + (t - j * a.B);
+}
+
+// One block's codes and scales of producer thread (token, side): of each pair
+// the 64 elements of slab 2 i + side, of the rope slab 32 elements.
+struct Codes {
+  uint4 c[4][2];
+  uint32_t s[4];
+  uint4 rc;
+  uint32_t rs;
+};
+
+template <int N, bool kQ4>
+__global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kernel(PagedAttendArgs a) {
+  using C = Shape<N, kQ4>;
+  constexpr int NC = C::kNC;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sb - raw);
+  float* run_max = reinterpret_cast<float*>(smem + C::kMiscOff);       // [2][N] log2 units
+  int32_t* row_pos = reinterpret_cast<int32_t*>(run_max + 2 * N);      // [2][N]
+  float* q_mul = reinterpret_cast<float*>(row_pos + 2 * N);            // [2][N] (4 bits)
+  float* warp_max = q_mul + 2 * N;                                     // [8][NC]
+  float* warp_sum = warp_max + 8 * NC;                                 // [8][NC]
+  float* row_inv = warp_sum + 8 * NC;                                  // [N]
+  Bars& B = *reinterpret_cast<Bars*>(smem + C::kBarOff);
+  volatile uint32_t* abort_flag = &B.abort;
+
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);
+  constexpr int kSoft0 = C::kProducers / 32, kMmaWarp = kSoft0 + kSoftWarps;
+  static_assert(kSoft0 % 4 == 0, "softmax warps start a TMEM lane quadrant");
+  auto fail = [&]() {
+    atomicOr(a.status, kErrTimeout);
+    *abort_flag = 1u;
+  };
+  if (tid == 0) {
+    mbar_init(&B.q_full, C::kProducers);
+    mbar_init(&B.q_free, 1);
+    mbar_init(&B.r_full, C::kProducers);
+    mbar_init(&B.r_free, 1);
+    mbar_init(&B.s_full, 1);
+    mbar_init(&B.p_full, kSoftThreads);
+    mbar_init(&B.o_done, 1);
+    mbar_init(&B.o_free, kSoftThreads);
+    mbar_init(&B.fin, 1);
+    for (int i = 0; i < kMaxRing; ++i) {
+      mbar_init(&B.e_full[i], C::kProducers);
+      mbar_init(&B.e_free[i], 1);
+    }
+    B.abort = 0u;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)),
+                 "r"(C::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(&B.tmem), 0);
+  // a warp's lanes wait together; false: the wait expired (or another role gave up)
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(kFull, mbar_wait(bar, parity & 1u, a.wait_ns)) && !__any_sync(kFull, *abort_flag != 0u);
+  };
+
+  Walk<N> walk;
+  walk.begin(a);
+  Seg s;
+  int g = 0;   // blocks so far
+  int tc = 0;  // segments with blocks so far
+
+  if (warp < kSoft0) {
+    if constexpr (!kQ4) {
+      // ---- producers, 16 bits -----------------------------------------------------------
+      bool ok = true;
+      while (ok && walk.next(a, s)) {
+        if (s.b0 >= s.b1) continue;
+        if (tc >= 1 && !wait(&B.q_free, (uint32_t)(tc - 1))) { fail(); break; }
+        const uint8_t* qsrc = reinterpret_cast<const uint8_t*>(a.q) + s.grow * kRowBytes16;
+        for (int i = tid; i < N * 72; i += C::kProducers) {
+          const int r = i / 72, c = i - r * 72;
+          const bool in = r < s.nrows;
+          cp_async16(swz(sb + C::kQOff + (uint32_t)(c >> 3) * C::kQSlab, r, c & 7),
+                     qsrc + (in ? (size_t)r * kRowBytes16 + c * 16 : 0), in);
+        }
+        cp_async_arrive_noinc(&B.q_full);
+        ++tc;
+        const int32_t* table = a.table + (int64_t)s.r * a.M;
+        for (int b = s.b0; b < s.b1; ++b, ++g) {
+          const int t0 = s.block(b) * kBlk;
+          // eight tokens from a multiple of 8 lie in one block of the cache: lane l < 16 looks up tokens t0 + 8 l..
+          int row8 = -1;
+          if (lane < 16 && t0 + 8 * lane <= s.pmax) row8 = (int)pool_row(a, table, t0 + 8 * lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int x = 4 * g + i, slot = x % C::kRing, use = x / C::kRing;
+            if (use >= 1 && !wait(&B.e_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
+            const uint32_t dst = sb + C::kRingOff + (uint32_t)slot * kPair;
+            const int c = tid & 15;
+#pragma unroll
+            for (int m = 0; m < 16; ++m) {
+              const int r = (tid >> 4) + 8 * m;
+              const int base = __shfl_sync(kFull, row8, m);
+              const bool in = base >= 0 && s.any_sees(t0 + r);
+              cp_async16(swz(dst + (uint32_t)(c >> 3) * kSlab, r, c & 7),
+                         a.pool + (in ? (int64_t)(base + (r & 7)) * kRowBytes16 + i * 256 + c * 16 : 0), in);
+            }
+            cp_async_arrive_noinc(&B.e_full[slot]);
+          }
+          if (!ok) break;
+          if (g >= 1 && !wait(&B.r_free, (uint32_t)(g - 1))) { ok = false; break; }
+          {
+            const int c = tid & 7;
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+              const int r = (tid >> 3) + 16 * m;
+              const int base = __shfl_sync(kFull, row8, r >> 3);
+              const bool in = base >= 0 && s.any_sees(t0 + r);
+              cp_async16(swz(sb + C::kRopeOff, r, c),
+                         a.pool + (in ? (int64_t)(base + (r & 7)) * kRowBytes16 + 1024 + c * 16 : 0), in);
+            }
+            cp_async_arrive_noinc(&B.r_full);
+          }
+        }
+        if (!ok) fail();
+      }
+      cp_async_wait_all();
+    } else {
+      // ---- producers, 4 bits ------------------------------------------------------------
+      const int tok = tid >> 1, side = tid & 1;
+      Codes k{};
+      const uint8_t *crow = nullptr, *srow = nullptr;  // null: zeros
+      auto locate = [&](const Seg& sg, int b) {
+        const int t = sg.block(b) * kBlk + tok;
+        const int64_t row = sg.any_sees(t) ? pool_row(a, a.table + (int64_t)sg.r * a.M, t) : -1;
+        crow = nullptr;
+        if (row >= 0) {
+          const int64_t blk = row / a.B;
+          const int in = (int)(row - blk * a.B);
+          const uint8_t* base = a.pool + blk * ((int64_t)a.B * kRowBytesQ4);
+          crow = base + (int64_t)in * kCodeBytes;
+          srow = base + (int64_t)a.B * kCodeBytes + in * kGroups;
+        }
+      };
+      auto load_pair = [&](int i) {
+        k.c[i][0] = k.c[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        k.s[i] = 0u;
+        if (crow) {
+          const uint4* p = reinterpret_cast<const uint4*>(crow + (2 * i + side) * 32);
+          k.c[i][0] = __ldg(p);
+          k.c[i][1] = __ldg(p + 1);
+          k.s[i] = __ldg(reinterpret_cast<const uint32_t*>(srow + (2 * i + side) * 4));
+        }
+      };
+      auto load_rope = [&]() {
+        k.rc = make_uint4(0u, 0u, 0u, 0u);
+        k.rs = 0u;
+        if (crow) {
+          k.rc = __ldg(reinterpret_cast<const uint4*>(crow + 256 + side * 16));
+          k.rs = __ldg(reinterpret_cast<const uint16_t*>(srow + 32 + side * 2));
+        }
+      };
+      bool ok = true, have = walk.next(a, s);
+      while (have && s.b0 >= s.b1) have = walk.next(a, s);
+      if (have) {
+        locate(s, s.b0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_pair(i);
+        load_rope();
+      }
+      while (ok && have) {
+        if (tc >= 1 && !wait(&B.q_free, (uint32_t)(tc - 1))) { fail(); break; }
+        // queries: one warp per row; scaled by 2^-e so that the largest magnitude is in [2^14, 2^15)
+        for (int r = warp; r < N; r += C::kProducers / 32) {
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + (s.grow + r) * kRow);
+          uint4 v[3];
+          uint32_t top = 0u;
+#pragma unroll
+          for (int m = 0; m < 3; ++m) {
+            const int c = lane + 32 * m;
+            v[m] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < s.nrows && c < 72) v[m] = __ldg(src + c);
+            const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) top = max(top, max(w[x] & 0x7fffu, (w[x] >> 16) & 0x7fffu));
+          }
+          top = __reduce_max_sync(kFull, top);
+          const int e = min(max((int)(top >> 7) - 127 - 14, -112), 112);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+          for (int m = 0; m < 3; ++m) {
+            const int c = lane + 32 * m;
+            if (c < 72) {
+              const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+              uint32_t h[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const __half2 p = __floats2half2_rn(bf_lo(w[x]) * down, bf_hi(w[x]) * down);
+                h[x] = *reinterpret_cast<const uint32_t*>(&p);
+              }
+              st_v4(swz(sb + C::kQOff + (uint32_t)(c >> 3) * C::kQSlab, r, c & 7), make_uint4(h[0], h[1], h[2], h[3]));
+            }
+          }
+          if (lane == 0) q_mul[(tc & 1) * N + r] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&B.q_full);
+        ++tc;
+        Seg nx = s;
+        bool more = true;
+        for (int b = s.b0; b < s.b1; ++b, ++g) {
+          // the block after this one, of this segment or of the next
+          bool pre = true;
+          if (b + 1 < s.b1) {
+            locate(s, b + 1);
+          } else {
+            do more = walk.next(a, nx); while (more && nx.b0 >= nx.b1);
+            pre = more;
+            if (more) locate(nx, nx.b0);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int x = 4 * g + i, slot = x % C::kRing, use = x / C::kRing;
+            if (use >= 1 && !wait(&B.e_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
+            const uint32_t dst = sb + C::kRingOff + (uint32_t)slot * kPair + (uint32_t)side * kSlab;
+            uint32_t sc[4];
+            scales2(k.s[i] & 0xffffu, sc[0], sc[1]);
+            scales2(k.s[i] >> 16, sc[2], sc[3]);
+            // a token's two threads start four chunks apart: the slabs are 16 KB apart, the same banks
+            const uint32_t cw[8] = {k.c[i][0].x, k.c[i][0].y, k.c[i][0].z, k.c[i][0].w,
+                                    k.c[i][1].x, k.c[i][1].y, k.c[i][1].z, k.c[i][1].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int o = side ? (q ^ 2) : q;
+              const uint32_t w0 = side ? cw[2 * (q ^ 2)] : cw[2 * q], w1 = side ? cw[2 * (q ^ 2) + 1] : cw[2 * q + 1];
+              uint4 lo, hi;
+              expand16(w0, w1, side ? sc[q ^ 2] : sc[q], lo, hi);
+              st_v4(swz(dst, tok, 2 * o), lo);
+              st_v4(swz(dst, tok, 2 * o + 1), hi);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&B.e_full[slot]);
+            if (pre) load_pair(i);
+          }
+          if (!ok) break;
+          if (g >= 1 && !wait(&B.r_free, (uint32_t)(g - 1))) { ok = false; break; }
+          {
+            uint32_t s0, s1;
+            scales2(k.rs, s0, s1);
+            uint4 lo, hi;
+            expand16(k.rc.x, k.rc.y, s0, lo, hi);
+            st_v4(swz(sb + C::kRopeOff, tok, 4 * side), lo);
+            st_v4(swz(sb + C::kRopeOff, tok, 4 * side + 1), hi);
+            expand16(k.rc.z, k.rc.w, s1, lo, hi);
+            st_v4(swz(sb + C::kRopeOff, tok, 4 * side + 2), lo);
+            st_v4(swz(sb + C::kRopeOff, tok, 4 * side + 3), hi);
+            fence_proxy_async_smem();
+            mbar_arrive(&B.r_full);
+            if (pre) load_rope();
+          }
+        }
+        if (!ok) fail();
+        s = nx;
+        have = more;
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- MMA issue ------------------------------------------------------------------------
+    const uint32_t el = elect();
+    constexpr uint32_t kIdS = idesc(!kQ4, kBlk, N, false, false);
+    constexpr uint32_t kIdO = idesc(!kQ4, kBlk, N, true, C::kSharedP);
+    const uint64_t ring_k = sdesc(sb + C::kRingOff, 16, 1024);      // K-major slabs
+    const uint64_t ring_v = sdesc(sb + C::kRingOff, kSlab, 1024);   // MN-major: two slabs, 128 value elements
+    const uint64_t rope = sdesc(sb + C::kRopeOff, 16, 1024);
+    const uint64_t qd = sdesc(sb + C::kQOff, 16, 1024);
+    const uint64_t pd = sdesc(sb + C::kPOff, 16, 1024);
+    bool ok = true;
+    while (ok && walk.next(a, s)) {
+      if (s.b0 >= s.b1) continue;
+      if (!wait(&B.q_full, (uint32_t)tc)) { ok = false; break; }
+      for (int b = s.b0; b < s.b1; ++b, ++g) {
+        const uint32_t dS = tmem + C::kColS;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = 4 * g + i, slot = x % C::kRing, use = x / C::kRing;
+          if (!wait(&B.e_full[slot], (uint32_t)use)) { ok = false; break; }
+          fence_proxy_async_smem();
+          tc_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss(dS, ring_k + (uint64_t)(((uint32_t)slot * kPair + (uint32_t)(kk >> 2) * kSlab) >> 4) + (uint64_t)((kk & 3) * 2),
+                   qd + (uint64_t)(((uint32_t)(2 * i + (kk >> 2)) * C::kQSlab) >> 4) + (uint64_t)((kk & 3) * 2), kIdS,
+                   (i | kk) ? 1u : 0u, el);
+        }
+        if (!ok || !wait(&B.r_full, (uint32_t)g)) { ok = false; break; }
+        fence_proxy_async_smem();
+        tc_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss(dS, rope + (uint64_t)(kk * 2), qd + (uint64_t)((8u * C::kQSlab) >> 4) + (uint64_t)(kk * 2), kIdS, 1u, el);
+        mma_commit(&B.s_full, el);
+        if (!C::kSharedP) mma_commit(&B.r_free, el);
+        if (b + 1 == s.b1) mma_commit(&B.q_free, el);
+        if (!wait(&B.p_full, (uint32_t)g)) { ok = false; break; }
+        if (b == s.b0 && tc >= 1 && !wait(&B.o_free, (uint32_t)(tc - 1))) { ok = false; break; }
+        fence_proxy_async_smem();
+        tc_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int slot = (4 * g + i) % C::kRing;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            // P^T: N = 64 MN-major (16 tokens are 2 KB), else K-major (64 tokens a slab of N rows)
+            const uint64_t p = C::kSharedP ? pd + (uint64_t)((uint32_t)kk * 2048u >> 4)
+                                           : pd + (uint64_t)(((uint32_t)(kk >> 2) * (N * 128u)) >> 4) + (uint64_t)((kk & 3) * 2);
+            mma_ss(tmem + (uint32_t)(i * N), ring_v + (uint64_t)(((uint32_t)slot * kPair + (uint32_t)kk * 2048u) >> 4), p, kIdO,
+                   (b > s.b0 || kk > 0) ? 1u : 0u, el);
+          }
+          mma_commit(&B.e_free[slot], el);
+        }
+        if (C::kSharedP) mma_commit(&B.r_free, el);
+        if (b + 1 == s.b1) mma_commit(&B.o_done, el);
+      }
+      ++tc;
+    }
+    if (!ok) fail();
+    // everything issued is complete before TMEM is freed (the tensor pipe waits on nothing outside this CTA)
+    mma_commit(&B.fin, el);
+    if (!__all_sync(kFull, mbar_wait(&B.fin, 0, a.wait_ns > 2000000000ull ? a.wait_ns : 2000000000ull))) fail();
+  } else {
+    // ---- softmax ---------------------------------------------------------------------------
+    const int st = tid - C::kProducers, sw = warp - kSoft0;
+    const int hw = sw >> 2, quad = sw & 3;            // half of the rows; lane quadrant
+    const int tok = 32 * quad + lane;                 // this thread's token of a block
+    const int c0 = hw * NC;                           // its first row of the tile
+    const uint32_t lane_addr = (uint32_t)(32 * quad) << 16;
+    const uint32_t bar_half = 2u + (uint32_t)hw;      // 128 threads with the same rows
+    bool ok = true;
+    while (ok && walk.next(a, s)) {
+      if (s.b0 >= s.b1) {  // nothing visible
+        for (int i = st; i < s.nrows * (kVal / 8); i += kSoftThreads)
+          reinterpret_cast<uint4*>(a.out + s.grow * kVal)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse && st < s.nrows) a.lse[s.grow + st] = -INFINITY;
+        continue;
+      }
+      float* mx = run_max + (tc & 1) * N;
+      int32_t* pos = row_pos + (tc & 1) * N;
+      if (st < N) {
+        mx[st] = kNone;
+        pos[st] = s.pos0 + (s.row0 + min(st, s.nrows - 1)) / s.H;
+      }
+      if (kQ4 && !wait(&B.q_full, (uint32_t)tc)) { ok = false; break; }  // the factors
+      named_sync(1, kSoftThreads);
+      const int32_t* table = a.table + (int64_t)s.r * a.M;
+      float l[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) l[c] = 0.f;
+      const bool many = s.pmin < s.pmax;
+      auto mapped = [&](int b) -> bool {
+        const int t = s.block(b) * kBlk + tok;
+        return b < s.b1 && s.any_sees(t) && pool_row(a, table, t) >= 0;
+      };
+      bool here_next = mapped(s.b0);
+      for (int b = s.b0; b < s.b1; ++b, ++g) {
+        const bool here = here_next;
+        here_next = mapped(b + 1);
+        if (!wait(&B.s_full, (uint32_t)g)) { ok = false; break; }
+        tc_after();
+        float v[NC];
+        tmem_ld<NC>(tmem + lane_addr + C::kColS + (uint32_t)c0, v);
+        tmem_wait_ld();
+        const int t = s.block(b) * kBlk + tok;
+        // the token is seen by every position of the tile, or by some
+        const bool all = here && t <= s.pmin && (a.window == 0 || t > s.pmax - a.window || t < s.snk);
+        const bool some = many && here && !all;
+        // scores in log2 units, less the running maximum; -inf where hidden
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float mul = kQ4 ? q_mul[(tc & 1) * N + c0 + c] : a.scale_log2;
+          const bool see = all || (some && t <= pos[c0 + c] && (a.window == 0 || t > pos[c0 + c] - a.window || t < s.snk));
+          v[c] = see ? v[c] * mul : -INFINITY;
+        }
+        bool over = b == s.b0;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) over = over || v[c] > mx[c0 + c] + kRescale;
+        if (named_any(bar_half, 128, over)) {
+          // the tokens' maximum of each row, then the running maximum, the sums and O^T move to it
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const uint32_t w = __reduce_max_sync(kFull, order_bits(fmaxf(v[c], -INFINITY)));
+            if (lane == 0) warp_max[sw * NC + c] = unorder_bits(w);
+          }
+          named_sync(bar_half, 128);
+          float fac[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float* wm = warp_max + 4 * hw * NC + c;
+            const float old = mx[c0 + c];
+            const float now = fmaxf(old, fmaxf(fmaxf(wm[0], wm[NC]), fmaxf(wm[2 * NC], wm[3 * NC])));
+            fac[c] = ex2(old - now);
+            l[c] *= fac[c];
+            if (quad == 0 && lane == 0) warp_sum[4 * hw * NC + c] = now;  // free until the tile's end
+          }
+          named_sync(bar_half, 128);
+          if (quad == 0 && lane < NC) mx[c0 + lane] = warp_sum[4 * hw * NC + lane];
+          if (b > s.b0) {
+            // s_full came after every earlier MMA, so O^T is at rest
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              float o[NC];
+              tmem_ld<NC>(tmem + lane_addr + (uint32_t)(i * N + c0), o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < NC; ++c) o[c] *= fac[c];
+#pragma unroll
+              for (int c = 0; c < NC; c += 8) tmem_st8(tmem + lane_addr + (uint32_t)(i * N + c0 + c), o + c);
+            }
+            tmem_wait_st();
+          }
+          named_sync(bar_half, 128);
+        }
+        // weights; the sum keeps them in fp32
+        uint32_t p[NC / 2];
+#pragma unroll
+        for (int c = 0; c < NC; c += 2) {
+          const float e0 = ex2(v[c] - (mx[c0 + c] - C::kBias)), e1 = ex2(v[c + 1] - (mx[c0 + c + 1] - C::kBias));
+          l[c] += e0;
+          l[c + 1] += e1;
+          if (kQ4) {
+            const __half2 h = __floats2half2_rn(e0, e1);
+            p[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
+            p[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        if (C::kSharedP) {  // [token][64 rows]
+#pragma unroll
+          for (int c = 0; c < NC / 8; ++c)
+            st_v4(swz(sb + C::kPOff, tok, c0 / 8 + c), make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]));
+        } else {  // [64 tokens of a slab] of each row
+          const uint32_t slab = sb + C::kPOff + (uint32_t)(tok >> 6) * (N * 128u);
+          const int in = tok & 63;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            st_u16(swz(slab, c0 + c, in >> 3) + (uint32_t)(in & 7) * 2u, (uint16_t)(p[c / 2] >> (16 * (c & 1))));
+        }
+        // A row that some positions of the tile see and others do not: its weight is 0 for the others, and 0
+        // times what is not finite would reach them.  Its values that are not finite become 0 here; where it is
+        // seen its score is not finite either.
+        uint32_t edge = __ballot_sync(kFull, some);
+        while (edge) {
+          const int r = 32 * quad + __ffs(edge) - 1;
+          edge &= edge - 1u;
+          // this half's two pairs: 32 chunks of 8 elements
+          const int i = 2 * hw + (lane >> 4), slot = (4 * g + i) % C::kRing;
+          const uint32_t at = swz(sb + C::kRingOff + (uint32_t)slot * kPair + (uint32_t)((lane >> 3) & 1) * kSlab, r, lane & 7);
+          const uint4 x = ld_v4(at);
+          constexpr uint32_t kExp = kQ4 ? 0x7c00u : 0x7f80u;
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((w[e] & kExp) == kExp) { w[e] &= 0xffff0000u; bad = true; }
+            if ((w[e] & (kExp << 16)) == (kExp << 16)) { w[e] &= 0x0000ffffu; bad = true; }
+          }
+          if (bad) st_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+        fence_proxy_async_smem();
+        tc_before();
+        mbar_arrive(&B.p_full);
+      }
+      if (!ok) break;
+      // sums over the tokens of each row
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float x = l[c];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+        if (lane == 0) warp_sum[sw * NC + c] = x;
+      }
+      named_sync(bar_half, 128);
+      if (quad == 0 && lane < NC) {
+        const float* ws = warp_sum + 4 * hw * NC + lane;
+        const float sum = (ws[0] + ws[NC]) + (ws[2 * NC] + ws[3 * NC]);
+        const int row = c0 + lane;
+        row_inv[row] = sum == 0.f ? 0.f : 1.f / sum;
+        if (s.part >= 0) {
+          float* ml = a.part_ml + ((int64_t)blockIdx.x * 2 + s.part) * 2 * N;
+          ml[row] = mx[row];
+          ml[N + row] = sum;
+        } else if (a.lse && row < s.nrows) {
+          a.lse[s.grow + row] = sum == 0.f ? -INFINITY : (mx[row] - C::kBias + log2f(sum)) * 0.6931471805599453f;
+        }
+      }
+      named_sync(bar_half, 128);
+      if (!wait(&B.o_done, (uint32_t)tc)) { ok = false; break; }
+      tc_after();
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        float o[NC];
+        tmem_ld<NC>(tmem + lane_addr + (uint32_t)(i * N + c0), o);
+        tmem_wait_ld();
+        const int e = i * 128 + tok;  // value element
+        if (s.part >= 0) {
+          float* dst = a.part_o + (((int64_t)blockIdx.x * 2 + s.part) * N + c0) * kVal + e;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if (c0 + c < s.nrows) dst[(size_t)c * kVal] = o[c];
+        } else {
+          // lanes 2 k and 2 k + 1 trade elements so that each stores a pair: the even one of row c, the odd one of c + 1
+          uint16_t* dst = a.out + (s.grow + c0) * kVal + (e & ~1);
+          const bool odd = lane & 1;
+#pragma unroll
+          for (int c = 0; c < NC; c += 2) {
+            const float x0 = o[c] * row_inv[c0 + c], x1 = o[c + 1] * row_inv[c0 + c + 1];
+            const float y = __shfl_xor_sync(kFull, odd ? x0 : x1, 1);
+            const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(y, x1) : __floats2bfloat162_rn(x0, y);
+            const int row = c + (odd ? 1 : 0);
+            if (c0 + row < s.nrows) *reinterpret_cast<__nv_bfloat162*>(dst + (size_t)row * kVal) = h;
+          }
+        }
+      }
+      tc_before();
+      mbar_arrive(&B.o_free);
+      ++tc;
+    }
+    if (!ok) fail();
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// join: one CTA per (tile, row) of a tile that several CTAs share; warp w takes
+// 128 value elements and every fourth part, and the four sums meet in shared
+// memory in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 512;
+
+template <int N>
+__global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArgs a, float bias) {
+  if (a.head[kHdListed] == 0) return;
+  __shared__ float4 acc[3][128];
+  __shared__ float wsum[4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int quarter = warp & 3, grp = warp >> 2;
+  const int used = a.head[kHdWorkers], n_tiles = a.head[kHdTiles];
+  // CTAs whose share starts inside a tile continue it: tile start[w].x is shared
+  // by the CTAs from the one before the first such w to the last
+  for (int item = blockIdx.x; item < used * N; item += gridDim.x) {
+    const int w0 = item / N, row = item - w0 * N;
+    // this item stands for the tile that CTA w0 leaves unfinished and begins (or is first to have blocks of)
+    if (w0 + 1 >= used) continue;
+    const int2 nx = a.start[w0 + 1];
+    if (nx.y <= kTileCost) continue;  // the next CTA starts a tile, or has all of its blocks
+    const int tile = nx.x;
+    const int2 me = a.start[w0];
+    // w0 is the tile's first CTA with blocks: its share starts before the tile's second block unit
+    if (!(me.x < tile || (me.x == tile && me.y <= kTileCost))) continue;
+    if (tile >= n_tiles) continue;
+    const int4 d = a.tiles[tile];
+    Seg s;
+    tile_of(a, N, d.x, d.y, s);
+    if (row >= s.nrows) continue;
+    int w1 = w0 + 1;  // last CTA with blocks of it
+    while (w1 + 1 < used && a.start[w1 + 1].x == tile) ++w1;
+    // w0's part: slot 1 when its share has the tile's own unit, else 0 (and so for every later one)
+    const int slot0 = me.x < tile || me.y < kTileCost ? 1 : 0;
+    float m = kNone;
+    for (int w = w0; w <= w1; ++w) m = fmaxf(m, a.part_ml[((int64_t)w * 2 + (w == w0 ? slot0 : 0)) * 2 * N + row]);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int w = w0 + grp; w <= w1; w += 4) {
+      const int64_t p = (int64_t)w * 2 + (w == w0 ? slot0 : 0);
+      const float f = ex2(a.part_ml[p * 2 * N + row] - m);
+      l += f * a.part_ml[p * 2 * N + N + row];
+      const float4 y = reinterpret_cast<const float4*>(a.part_o + (p * N + row) * kVal)[quarter * 32 + lane];
+      x.x += f * y.x;
+      x.y += f * y.y;
+      x.z += f * y.z;
+      x.w += f * y.w;
+    }
+    __syncthreads();
+    if (grp > 0) acc[grp - 1][quarter * 32 + lane] = x;
+    if (lane == 0 && quarter == 0) wsum[grp] = l;
+    __syncthreads();
+    if (grp == 0) {
+      const float L = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const float4 y = acc[k][quarter * 32 + lane];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const __nv_bfloat162 h0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), h1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+      reinterpret_cast<uint2*>(a.out + (s.grow + row) * kVal)[quarter * 32 + lane] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+      if (tid == 0 && a.lse) a.lse[s.grow + row] = L == 0.f ? -INFINITY : (m - bias + log2f(L)) * 0.6931471805599453f;
+    }
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <int N, bool kQ4>
+cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
+  using C = Shape<N, kQ4>;
+  cudaError_t e = cudaFuncSetAttribute(attend_paged_kernel<N, kQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  schedule_paged_kernel<<<1, kSchedThreads, 0, s>>>(a, N);
+  attend_paged_kernel<N, kQ4><<<a.workers, C::kThreads, C::kSmem, s>>>(a);
+  join_paged_kernel<N><<<2 * a.workers, kJoinThreads, 0, s>>>(a, C::kBias);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Rows per tile: the mean rows of a request, up to 64.
+int paged_tile_rows(int n_requests, int n_tokens, int H) {
+  const int64_t rows = ((int64_t)n_tokens + n_requests - 1) / n_requests * H;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+size_t paged_attend_workspace(int n_requests, int n_tokens, int H, int workers) {
+  const size_t N = (size_t)paged_tile_rows(n_requests, n_tokens, H), W = (size_t)workers;
+  return 256 + up256(((size_t)n_requests + 1) * 4) + up256(kListTiles * sizeof(int4)) + up256((W + 1) * sizeof(int2)) +
+         up256(W * 4 * N * 4) + W * 2 * N * kVal * 4;
+}
+void paged_attend_carve(PagedAttendArgs& a, uint8_t* w) {
+  const size_t N = (size_t)paged_tile_rows(a.R, a.n_tokens, a.H), W = (size_t)a.workers;
+  a.head = reinterpret_cast<int32_t*>(w);
+  if (!a.status) a.status = reinterpret_cast<uint32_t*>(w + 64);
+  w += 256;
+  a.tile_off = reinterpret_cast<int32_t*>(w);
+  w += up256(((size_t)a.R + 1) * 4);
+  a.tiles = reinterpret_cast<int4*>(w);
+  w += up256(kListTiles * sizeof(int4));
+  a.start = reinterpret_cast<int2*>(w);
+  w += up256((W + 1) * sizeof(int2));
+  a.part_ml = reinterpret_cast<float*>(w);
+  w += up256(W * 4 * N * 4);
+  a.part_o = reinterpret_cast<float*>(w);
+}
+cudaError_t launch_paged_attend(const PagedAttendArgs& a, bool q4, cudaStream_t s) {
+  const int N = paged_tile_rows(a.R, a.n_tokens, a.H);
+  if (q4) return N == 16 ? launch<16, true>(a, s) : N == 32 ? launch<32, true>(a, s) : launch<64, true>(a, s);
+  return N == 16 ? launch<16, false>(a, s) : N == 32 ? launch<32, false>(a, s) : launch<64, false>(a, s);
+}
+
+}  // namespace kvo

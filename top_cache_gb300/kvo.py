@@ -44,13 +44,16 @@ KVO_IDX_BF16 = 0
 KVO_IDX_INT8 = 1
 KVO_GATHER_LDG = 0
 KVO_GATHER_BULK = 1
+KVO_CACHE_BF16 = 0
+KVO_CACHE_Q4 = 1
 
 EXPORTED = ("kvo_create", "kvo_destroy", "kvo_host_rows", "kvo_prefill", "kvo_append", "kvo_step",
             "kvo_select_workspace_size", "kvo_select", "kvo_reset", "kvo_profile_read",
             "kvo_set_option", "kvo_get_option", "kvo_get_stats", "kvo_export_state", "kvo_select_noalloc",
             "kvo_attend", "kvo_set_blocks", "kvo_host_block", "kvo_wait_selftest", "kvo_lw_create", "kvo_lw_destroy", "kvo_lw_plan", "kvo_lw_host_rows",
             "kvo_lw_set_length", "kvo_lw_begin", "kvo_lw_layer", "kvo_lw_layer_done", "kvo_lw_end",
-            "kvo_lw_stats", "kvo_last_error")
+            "kvo_lw_stats", "kvo_last_error", "kvo_paged_block_bytes", "kvo_paged_plan", "kvo_paged_write",
+            "kvo_paged_read", "kvo_paged_attend_workspace_size", "kvo_paged_attend")
 
 
 class KvoConfig(ctypes.Structure):
@@ -161,6 +164,20 @@ def lib():
             L.kvo_lw_end.argtypes = [vp, vp]
             L.kvo_lw_stats.restype = ctypes.c_int
             L.kvo_lw_stats.argtypes = [vp, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)]
+            L.kvo_paged_block_bytes.restype = i64
+            L.kvo_paged_block_bytes.argtypes = [i32, i32]
+            L.kvo_paged_plan.restype = ctypes.c_int
+            L.kvo_paged_plan.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp,
+                                         i32, vp, vp]
+            L.kvo_paged_write.restype = ctypes.c_int
+            L.kvo_paged_write.argtypes = [vp, vp, i64, vp, i64, i32, i32, vp]
+            L.kvo_paged_read.restype = ctypes.c_int
+            L.kvo_paged_read.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp]
+            L.kvo_paged_attend_workspace_size.restype = ctypes.c_size_t
+            L.kvo_paged_attend_workspace_size.argtypes = [i32, i32, i32, i32]
+            L.kvo_paged_attend.restype = ctypes.c_int
+            L.kvo_paged_attend.argtypes = [vp, i64, i32, i32, vp, i32, vp, vp, i32, vp, i32, i32,
+                                           ctypes.c_float, i32, i32, vp, vp, vp, ctypes.c_size_t, vp, vp]
             _lib = L
     return _lib
 
@@ -319,6 +336,157 @@ def kvo_export_state(h, unit, max_tokens, capacity, row_elems=576, with_rows=Fal
                                   hot.ctypes.data if with_rows else None))
     return {"cache_slots": cs, "slot_token": st, "last_use": lu, "length": ln.value,
             "stamp": sp.value, "hot": hot}
+
+
+def _tensor(t, name, dtype, device, shape=None):
+    """Address of a dense device tensor of the given type; shape entries of None are free."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise KvoError(KVO_EINVAL, "%s must be a CUDA tensor" % name)
+    if device is not None and t.device != device:
+        raise KvoError(KVO_EINVAL, "%s is on %s, not on %s" % (name, t.device, device))
+    if (t.dtype is not dtype) if not isinstance(dtype, tuple) else (t.dtype not in dtype):
+        raise KvoError(KVO_EINVAL, "%s has type %s" % (name, t.dtype))
+    if shape is not None:
+        have = t.shape
+        if len(have) != len(shape) or any(n is not None and n != m for n, m in zip(shape, have)):
+            raise KvoError(KVO_EINVAL, "%s has shape %s, not %s" % (name, tuple(have), shape))
+    if not t.is_contiguous():
+        raise KvoError(KVO_EINVAL, "%s is not contiguous" % name)
+    return t.data_ptr()
+
+
+def _on(device, stream, call):
+    """call(stream handle) with `device` current (the launches go there)."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return _check(call(_stream(stream)))
+    with torch.cuda.device(device):
+        return _check(call(_stream(stream)))
+
+
+def _types16():
+    import torch
+    return (torch.bfloat16, torch.int16)  # int16: bf16 bits, as elsewhere in this binding
+
+
+def _pool(pool, n_blocks, block_tokens, format):
+    """Address and device of a cache's pool, whose bytes must hold n_blocks blocks."""
+    import torch
+    size = kvo_paged_block_bytes(format, block_tokens)
+    p = _tensor(pool, "pool", (torch.uint8, torch.bfloat16, torch.int16), None)
+    if pool.numel() * pool.element_size() < n_blocks * size:
+        raise KvoError(KVO_EINVAL, "pool is smaller than n_blocks blocks")
+    return p, pool.device
+
+
+def kvo_paged_block_bytes(format, block_tokens):
+    """Bytes of one block of a paged device cache (KVO_CACHE_BF16 or KVO_CACHE_Q4)."""
+    n = int(lib().kvo_paged_block_bytes(format, block_tokens))
+    if n == 0:
+        raise KvoError(KVO_EINVAL, "unknown cache format, or block_tokens not a multiple of 8 in 8 .. 65536")
+    return n
+
+
+def kvo_paged_plan(lengths, new_tokens, block_tokens, block_table, ring, ring_in, ring_out, lengths_out, kv_lens,
+                   cu_new, slots, status, window=0, sinks=0, stream=None):
+    """Block tables and the slot map of a step, built on the device (see kvo.h).
+
+    int32 CUDA tensors: lengths, new_tokens, lengths_out, kv_lens, status [R], block_table [R][max_blocks],
+    ring [ring_size], cu_new [R + 1], slots [n_slots]; int64 [2]: ring_in, ring_out.
+    """
+    import torch
+    i32, i64 = torch.int32, torch.int64
+    a = _tensor(lengths, "lengths", i32, None, (None,))
+    dev, R = lengths.device, lengths.shape[0]
+    one = (R,)
+    b = _tensor(new_tokens, "new_tokens", i32, dev, one)
+    t = _tensor(block_table, "block_table", i32, dev, (R, None))
+    f = _tensor(ring, "ring", i32, dev, (None,))
+    fi = _tensor(ring_in, "ring_in", i64, dev, (2,))
+    fo = _tensor(ring_out, "ring_out", i64, dev, (2,))
+    lo = _tensor(lengths_out, "lengths_out", i32, dev, one)
+    kv = _tensor(kv_lens, "kv_lens", i32, dev, one)
+    cu = _tensor(cu_new, "cu_new", i32, dev, (R + 1,))
+    sl = _tensor(slots, "slots", i32, dev, (None,))
+    st = _tensor(status, "status", i32, dev, one)
+    M, F, S = block_table.shape[1], ring.shape[0], slots.shape[0]
+    f_ = lib().kvo_paged_plan
+    return _on(dev, stream, lambda s: f_(a, b, R, block_tokens, M, window, sinks, t, f, F, fi, fo, lo, kv, cu, sl, S,
+                                         st, s))
+
+
+def kvo_paged_write(rows, slots, pool, n_blocks, block_tokens, format, stream=None):
+    """Rows (bf16 [n][576]) into the cache at slots (int32 [n], below 0: skipped)."""
+    import torch
+    p, dev = _pool(pool, n_blocks, block_tokens, format)
+    r = _tensor(rows, "rows", _types16(), dev, (None, 576))
+    n = rows.shape[0]
+    s = _tensor(slots, "slots", torch.int32, dev, (n,))
+    return _on(dev, stream, lambda st: lib().kvo_paged_write(r, s, n, p, n_blocks, block_tokens, format, st))
+
+
+def kvo_paged_read(pool, n_blocks, block_tokens, format, slots, rows, stream=None):
+    """The cache's values at slots (int32 [n]) into rows (bf16 [n][576]); skipped rows stay as they were."""
+    import torch
+    p, dev = _pool(pool, n_blocks, block_tokens, format)
+    r = _tensor(rows, "rows", _types16(), dev, (None, 576))
+    n = rows.shape[0]
+    s = _tensor(slots, "slots", torch.int32, dev, (n,))
+    return _on(dev, stream, lambda st: lib().kvo_paged_read(p, n_blocks, block_tokens, format, s, n, r, st))
+
+
+_attend_sizes = {}
+
+
+def kvo_paged_attend_workspace_size(n_requests, n_tokens, n_heads, device=0):
+    key = (n_requests, n_tokens, n_heads, device)
+    n = _attend_sizes.get(key)
+    if n is None:
+        n = int(lib().kvo_paged_attend_workspace_size(n_requests, n_tokens, n_heads, device))
+        if len(_attend_sizes) >= 4096:
+            _attend_sizes.clear()
+        if n:
+            _attend_sizes[key] = n
+    return n
+
+
+def kvo_paged_attend(pool, n_blocks, block_tokens, format, block_table, kv_lens, cu_tokens, queries, scale, out,
+                     lse=None, window=0, sinks=0, workspace=None, status=None, stream=None):
+    """Attention of queries (bf16 [T][H][576]) over the cache into out (bf16 [T][H][512]) and lse (float32 [T][H]
+    or None); request r's tokens are cu_tokens[r] .. cu_tokens[r + 1] - 1 (int32 [R + 1]) and its cache has
+    kv_lens[r] tokens (int32 [R]) through block_table (int32 [R][max_blocks]).
+
+    workspace: uint8 CUDA tensor of kvo_paged_attend_workspace_size bytes; by default one is taken from the
+    caching allocator on the stream of the call.
+    """
+    import torch
+    p, dev = _pool(pool, n_blocks, block_tokens, format)
+    i32 = torch.int32
+    kv = _tensor(kv_lens, "kv_lens", i32, dev, (None,))
+    R = kv_lens.shape[0]
+    t = _tensor(block_table, "block_table", i32, dev, (R, None))
+    cu = _tensor(cu_tokens, "cu_tokens", i32, dev, (R + 1,))
+    q = _tensor(queries, "queries", _types16(), dev, (None, None, 576))
+    T, H = queries.shape[0], queries.shape[1]
+    o = _tensor(out, "out", _types16(), dev, (T, H, 512))
+    e = None if lse is None else _tensor(lse, "lse", torch.float32, dev, (T, H))
+    st = None if status is None else _tensor(status, "status", (i32, torch.uint32), dev, (1,))
+    size = kvo_paged_attend_workspace_size(R, T, H, dev.index)
+    if workspace is None:
+        if stream is not None and _stream(stream) != torch.cuda.current_stream(dev).cuda_stream:
+            # memory of the caching allocator belongs to the stream that it was taken on
+            if isinstance(stream, int):
+                raise KvoError(KVO_EINVAL, "a raw stream that is not the current one needs a workspace")
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        else:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    w = _tensor(workspace, "workspace", torch.uint8, dev, (None,))
+    M, n_w = block_table.shape[1], workspace.shape[0]
+    f = lib().kvo_paged_attend
+    return _on(dev, stream, lambda s: f(p, n_blocks, block_tokens, format, t, M, kv, cu, R, q, T, H, float(scale),
+                                        window, sinks, o, e, w, n_w, st, s))
 
 
 class Kvo:
