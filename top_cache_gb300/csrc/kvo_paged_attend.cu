@@ -25,11 +25,11 @@
 //   producers    the tile's queries, then each block's rows into a ring of
 //                pairs of 128-byte-swizzled K-major slabs (128 tokens x 64
 //                elements); the same bytes are the K-major A of S^T and the
-//                MN-major A of O^T.  16 bits: 4 warps, 16-byte cp.async (a row
-//                not to be read is zero-filled).  4 bits: 8 warps hold the next
-//                block's codes in registers while they expand this one's to
-//                fp16 (exact; queries are scaled by a power of two per row to
-//                fit fp16, undone in the scores)
+//                MN-major A of O^T.  16 bits: one warp, a lane per TMA box of
+//                64 elements x the rows of one cache block (runs of 8 to 128).
+//                4 bits: 8 warps hold the next block's codes in registers while
+//                they expand this one's to fp16 (exact; queries are scaled by a
+//                power of two per row to fit fp16, undone in the scores)
 //   softmax      8 warps, one token (TMEM lane) per thread and half of the
 //                tile's rows.  Per-thread sums; a running maximum that moves
 //                only when a score passes it by 2^8, so most blocks need no
@@ -44,10 +44,13 @@
 // alone leaves partial (O, m, l) in the workspace, at most two per CTA, and a
 // third kernel joins them in CTA order.  Many tiles: CTA c takes tiles c, c +
 // CTAs, ... whole (neighbours cost alike).  Results do not depend on timing.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "kvo_paged.cuh"
 
@@ -72,8 +75,10 @@ constexpr float kRescale = 8.f;              // log2: how far a score may pass t
 
 template <int N, bool kQ4>
 struct Shape {
-  static constexpr int kProducers = kQ4 ? 256 : 128;
-  static constexpr int kThreads = kProducers + kSoftThreads + 32;
+  static constexpr int kProdWarps = kQ4 ? 8 : 1;
+  static constexpr int kProducers = kProdWarps * 32;
+  static constexpr int kFillers = kQ4 ? kProducers : 1;  // arrivals that complete a filled slot
+  static constexpr int kThreads = kSoftThreads + kProducers + 32;
   static constexpr int kNC = N / 2;                    // rows of one softmax thread
   static constexpr bool kSharedP = N == 64;            // P^T lies in the rope slab's place
   static constexpr int kRing = N == 64 ? 4 : kMaxRing; // pairs
@@ -84,15 +89,17 @@ struct Shape {
   static constexpr uint32_t kPOff = kSharedP ? kRopeOff : kRopeOff + kSlab;
   static constexpr uint32_t kPBytes = kSharedP ? 0u : N * 256u;
   static constexpr uint32_t kMiscOff = kRopeOff + kSlab + kPBytes;
-  // misc: running maxima, row positions and query factors [2][N], warp maxima and sums [8][NC], 1 / l [N]
-  static constexpr uint32_t kMiscBytes = (3 * 2 * N + 2 * 8 * kNC + N) * 4;
+  // misc: less running maxima, query factors, row positions [2][N], a block's maxima and the tile's sums [8][NC],
+  // factors of a move of the running maximum [N], 1 / l [N]
+  static constexpr uint32_t kMiscBytes = (3 * 2 * N + 2 * 8 * kNC + 2 * N) * 4;
   static constexpr uint32_t kBarOff = kMiscOff + kMiscBytes;
   static constexpr uint32_t kSmem = kBarOff + 256 + 1024;  // barriers and flags, alignment slack
   static constexpr uint32_t kTmem = N == 64 ? 512 : N == 32 ? 256 : 128;
   static constexpr uint32_t kColS = 4 * N;             // O^T: value elements 128 i.. at columns i * N
   static constexpr float kBias = kQ4 ? 7.f : 0.f;      // P is 2^kBias exp2(..): keeps small weights out of fp16's subnormals
   static_assert(kSmem <= 232448, "shared memory of one CTA");
-  static_assert(kRingOff % 1024 == 0 && kPOff % 1024 == 0 && kBarOff % 8 == 0, "swizzled tiles sit on 1 KB boundaries");
+  static_assert(kRingOff % 1024 == 0 && kPOff % 1024 == 0 && kMiscOff % 16 == 0 && kBarOff % 8 == 0,
+                "swizzled tiles sit on 1 KB boundaries");
 };
 
 // ---- tcgen05 ------------------------------------------------------------------------------
@@ -159,13 +166,12 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[NC]) {
 __device__ __forceinline__ uint32_t swz(uint32_t slab, int r, int c) {
   return slab + (uint32_t)r * 128u + ((uint32_t)(c ^ (r & 7)) << 4);
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// One arrival once every cp.async that this thread has issued so far has landed.
-__device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+// A box of a 2-D tensor map (x: element, y: row), completion counted in bytes on bar.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void st_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -422,35 +428,43 @@ struct Codes {
   uint32_t rs;
 };
 
+// 16 bits: the pool's rows in boxes of 64 elements x `run` rows (the largest
+// power of two, at most 128, that divides block_tokens), the queries' in 64 x N.
+struct Maps {
+  CUtensorMap pool, q;
+  int run;
+};
+
 template <int N, bool kQ4>
-__global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kernel(PagedAttendArgs a) {
+__global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
+    attend_paged_kernel(PagedAttendArgs a, const __grid_constant__ Maps maps) {
   using C = Shape<N, kQ4>;
   constexpr int NC = C::kNC;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sb = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sb - raw);
-  float* run_max = reinterpret_cast<float*>(smem + C::kMiscOff);       // [2][N] log2 units
-  int32_t* row_pos = reinterpret_cast<int32_t*>(run_max + 2 * N);      // [2][N]
-  float* q_mul = reinterpret_cast<float*>(row_pos + 2 * N);            // [2][N] (4 bits)
-  float* warp_max = q_mul + 2 * N;                                     // [8][NC]
+  float* less_max = reinterpret_cast<float*>(smem + C::kMiscOff);      // [2][N] kBias - running maximum (log2 units)
+  float* q_mul = less_max + 2 * N;                                     // [2][N] (4 bits)
+  int32_t* row_pos = reinterpret_cast<int32_t*>(q_mul + 2 * N);        // [2][N]
+  float* warp_max = reinterpret_cast<float*>(row_pos + 2 * N);         // [8][NC]
   float* warp_sum = warp_max + 8 * NC;                                 // [8][NC]
-  float* row_inv = warp_sum + 8 * NC;                                  // [N]
+  float* move_by = warp_sum + 8 * NC;                                  // [N]
+  float* row_inv = move_by + N;                                        // [N]
   Bars& B = *reinterpret_cast<Bars*>(smem + C::kBarOff);
   volatile uint32_t* abort_flag = &B.abort;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);
-  constexpr int kSoft0 = C::kProducers / 32, kMmaWarp = kSoft0 + kSoftWarps;
-  static_assert(kSoft0 % 4 == 0, "softmax warps start a TMEM lane quadrant");
+  constexpr int kProd0 = kSoftWarps, kMmaWarp = kProd0 + C::kProdWarps;  // softmax warps first: whole TMEM lane quadrants
   auto fail = [&]() {
     atomicOr(a.status, kErrTimeout);
     *abort_flag = 1u;
   };
   if (tid == 0) {
-    mbar_init(&B.q_full, C::kProducers);
+    mbar_init(&B.q_full, C::kFillers);
     mbar_init(&B.q_free, 1);
-    mbar_init(&B.r_full, C::kProducers);
+    mbar_init(&B.r_full, C::kFillers);
     mbar_init(&B.r_free, 1);
     mbar_init(&B.s_full, 1);
     mbar_init(&B.p_full, kSoftThreads);
@@ -458,7 +472,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
     mbar_init(&B.o_free, kSoftThreads);
     mbar_init(&B.fin, 1);
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&B.e_full[i], C::kProducers);
+      mbar_init(&B.e_full[i], C::kFillers);
       mbar_init(&B.e_free[i], 1);
     }
     B.abort = 0u;
@@ -485,65 +499,62 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
   int g = 0;   // blocks so far
   int tc = 0;  // segments with blocks so far
 
-  if (warp < kSoft0) {
+  if (warp >= kProd0 && warp < kMmaWarp) {
     if constexpr (!kQ4) {
-      // ---- producers, 16 bits -----------------------------------------------------------
+      // ---- producer, 16 bits --------------------------------------------------------------
+      const int run = maps.run, runs = kBlk / run;
+      int pairs = 0, ropes = 0;  // filled, or being filled
       bool ok = true;
       while (ok && walk.next(a, s)) {
         if (s.b0 >= s.b1) continue;
-        if (tc >= 1 && !wait(&B.q_free, (uint32_t)(tc - 1))) { fail(); break; }
-        const uint8_t* qsrc = reinterpret_cast<const uint8_t*>(a.q) + s.grow * kRowBytes16;
-        for (int i = tid; i < N * 72; i += C::kProducers) {
-          const int r = i / 72, c = i - r * 72;
-          const bool in = r < s.nrows;
-          cp_async16(swz(sb + C::kQOff + (uint32_t)(c >> 3) * C::kQSlab, r, c & 7),
-                     qsrc + (in ? (size_t)r * kRowBytes16 + c * 16 : 0), in);
-        }
-        cp_async_arrive_noinc(&B.q_full);
+        if (tc >= 1 && !wait(&B.q_free, (uint32_t)(tc - 1))) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(&B.q_full, kSlabs * C::kQSlab);
+        __syncwarp();
+        // rows behind the tile's are the next ones' or zeros, and go nowhere
+        if (lane < kSlabs) tma_box(sb + C::kQOff + (uint32_t)lane * C::kQSlab, &maps.q, 64 * lane, (int)s.grow, &B.q_full);
         ++tc;
         const int32_t* table = a.table + (int64_t)s.r * a.M;
+        // lane l holds the pool row of the block's run l / 2 (-1: not read), of the next block while this one's is issued
+        auto find = [&](int b) -> int {
+          const int t = s.block(b) * kBlk + (lane >> 1) * run;
+          if ((lane >> 1) >= runs || t > s.pmax || (t + run - 1 < s.lo && t >= s.snk)) return -1;
+          return (int)pool_row(a, table, t);
+        };
+        int next = find(s.b0);
         for (int b = s.b0; b < s.b1; ++b, ++g) {
-          const int t0 = s.block(b) * kBlk;
-          // eight tokens from a multiple of 8 lie in one block of the cache: lane l < 16 looks up tokens t0 + 8 l..
-          int row8 = -1;
-          if (lane < 16 && t0 + 8 * lane <= s.pmax) row8 = (int)pool_row(a, table, t0 + 8 * lane);
+          const int row = next;
+          if (b + 1 < s.b1) next = find(b + 1);
+          const uint32_t got = __popc(__ballot_sync(kFull, row >= 0)) >> 1;  // runs
+          const uint32_t off = (uint32_t)((lane >> 1) * run) * 128u;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int x = 4 * g + i, slot = x % C::kRing, use = x / C::kRing;
             if (use >= 1 && !wait(&B.e_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
-            const uint32_t dst = sb + C::kRingOff + (uint32_t)slot * kPair;
-            const int c = tid & 15;
-#pragma unroll
-            for (int m = 0; m < 16; ++m) {
-              const int r = (tid >> 4) + 8 * m;
-              const int base = __shfl_sync(kFull, row8, m);
-              const bool in = base >= 0 && s.any_sees(t0 + r);
-              cp_async16(swz(dst + (uint32_t)(c >> 3) * kSlab, r, c & 7),
-                         a.pool + (in ? (int64_t)(base + (r & 7)) * kRowBytes16 + i * 256 + c * 16 : 0), in);
-            }
-            cp_async_arrive_noinc(&B.e_full[slot]);
+            if (lane == 0) mbar_arrive_expect_tx(&B.e_full[slot], got * 2u * (uint32_t)run * 128u);
+            __syncwarp();
+            pairs = x + 1;
+            if (row >= 0)
+              tma_box(sb + C::kRingOff + (uint32_t)slot * kPair + (uint32_t)(lane & 1) * kSlab + off, &maps.pool,
+                      128 * i + 64 * (lane & 1), row, &B.e_full[slot]);
           }
           if (!ok) break;
           if (g >= 1 && !wait(&B.r_free, (uint32_t)(g - 1))) { ok = false; break; }
-          {
-            const int c = tid & 7;
-#pragma unroll
-            for (int m = 0; m < 8; ++m) {
-              const int r = (tid >> 3) + 16 * m;
-              const int base = __shfl_sync(kFull, row8, r >> 3);
-              const bool in = base >= 0 && s.any_sees(t0 + r);
-              cp_async16(swz(sb + C::kRopeOff, r, c),
-                         a.pool + (in ? (int64_t)(base + (r & 7)) * kRowBytes16 + 1024 + c * 16 : 0), in);
-            }
-            cp_async_arrive_noinc(&B.r_full);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&B.r_full, got * (uint32_t)run * 128u);
+          __syncwarp();
+          ropes = g + 1;
+          if (row >= 0 && !(lane & 1)) tma_box(sb + C::kRopeOff + off, &maps.pool, kVal, row, &B.r_full);
         }
-        if (!ok) fail();
       }
-      cp_async_wait_all();
+      if (!ok) fail();
+      // the CTA may not end before its copies have landed (they have, unless a role gave up)
+      bool landed = tc == 0 || mbar_wait(&B.q_full, (uint32_t)(tc - 1) & 1u, a.wait_ns);
+      if (ropes > 0) landed = mbar_wait(&B.r_full, (uint32_t)(ropes - 1) & 1u, a.wait_ns) && landed;
+      for (int x = max(0, pairs - C::kRing); x < pairs; ++x)
+        landed = mbar_wait(&B.e_full[x % C::kRing], (uint32_t)(x / C::kRing) & 1u, a.wait_ns) && landed;
+      if (!landed) fail();
     } else {
       // ---- producers, 4 bits ------------------------------------------------------------
-      const int tok = tid >> 1, side = tid & 1;
+      const int pt = tid - kSoftThreads, tok = pt >> 1, side = pt & 1;
       Codes k{};
       const uint8_t *crow = nullptr, *srow = nullptr;  // null: zeros
       auto locate = [&](const Seg& sg, int b) {
@@ -587,7 +598,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
       while (ok && have) {
         if (tc >= 1 && !wait(&B.q_free, (uint32_t)(tc - 1))) { fail(); break; }
         // queries: one warp per row; scaled by 2^-e so that the largest magnitude is in [2^14, 2^15)
-        for (int r = warp; r < N; r += C::kProducers / 32) {
+        for (int r = warp - kProd0; r < N; r += C::kProdWarps) {
           const uint4* src = reinterpret_cast<const uint4*>(a.q + (s.grow + r) * kRow);
           uint4 v[3];
           uint32_t top = 0u;
@@ -745,12 +756,12 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
     if (!__all_sync(kFull, mbar_wait(&B.fin, 0, a.wait_ns > 2000000000ull ? a.wait_ns : 2000000000ull))) fail();
   } else {
     // ---- softmax ---------------------------------------------------------------------------
-    const int st = tid - C::kProducers, sw = warp - kSoft0;
-    const int hw = sw >> 2, quad = sw & 3;            // half of the rows; lane quadrant
-    const int tok = 32 * quad + lane;                 // this thread's token of a block
-    const int c0 = hw * NC;                           // its first row of the tile
+    const int st = tid, hw = warp >> 2, quad = warp & 3;  // half of the rows; lane quadrant
+    const int tok = 32 * quad + lane;                     // this thread's token of a block
+    const int c0 = hw * NC;                               // its first row of the tile
     const uint32_t lane_addr = (uint32_t)(32 * quad) << 16;
-    const uint32_t bar_half = 2u + (uint32_t)hw;      // 128 threads with the same rows
+    const uint32_t sS = tmem + lane_addr + C::kColS + (uint32_t)c0;
+    const uint32_t bar_half = 2u + (uint32_t)hw;          // 128 threads with the same rows
     bool ok = true;
     while (ok && walk.next(a, s)) {
       if (s.b0 >= s.b1) {  // nothing visible
@@ -759,10 +770,11 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
         if (a.lse && st < s.nrows) a.lse[s.grow + st] = -INFINITY;
         continue;
       }
-      float* mx = run_max + (tc & 1) * N;
+      float* lm = less_max + (tc & 1) * N;
       int32_t* pos = row_pos + (tc & 1) * N;
+      const float* qm = q_mul + (tc & 1) * N;
       if (st < N) {
-        mx[st] = kNone;
+        lm[st] = C::kBias - kNone;
         pos[st] = s.pos0 + (s.row0 + min(st, s.nrows - 1)) / s.H;
       }
       if (kQ4 && !wait(&B.q_full, (uint32_t)tc)) { ok = false; break; }  // the factors
@@ -771,7 +783,6 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
       float l[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) l[c] = 0.f;
-      const bool many = s.pmin < s.pmax;
       auto mapped = [&](int b) -> bool {
         const int t = s.block(b) * kBlk + tok;
         return b < s.b1 && s.any_sees(t) && pool_row(a, table, t) >= 0;
@@ -780,66 +791,93 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
       for (int b = s.b0; b < s.b1; ++b, ++g) {
         const bool here = here_next;
         here_next = mapped(b + 1);
-        if (!wait(&B.s_full, (uint32_t)g)) { ok = false; break; }
-        tc_after();
-        float v[NC];
-        tmem_ld<NC>(tmem + lane_addr + C::kColS + (uint32_t)c0, v);
-        tmem_wait_ld();
         const int t = s.block(b) * kBlk + tok;
         // the token is seen by every position of the tile, or by some
         const bool all = here && t <= s.pmin && (a.window == 0 || t > s.pmax - a.window || t < s.snk);
-        const bool some = many && here && !all;
-        // scores in log2 units, less the running maximum; -inf where hidden
+        const bool some = here && !all;
+        const bool plain = __all_sync(kFull, all);
+        if (!wait(&B.s_full, (uint32_t)g)) { ok = false; break; }
+        tc_after();
+        float v[NC];
+        // v: scores in log2 units less the running maximum (plus kBias); -inf where hidden.  Where the maximum has
+        // just moved the product is rounded as the maximum was, so that its own score is no less than 0 however
+        // large it is; else the two are fused.
+        auto scores = [&](auto fused) {
+          auto less = [&](float x, float m, float y) {
+            return decltype(fused)::value ? fmaf(x, m, y) : __fadd_rn(__fmul_rn(x, m), y);
+          };
+          tmem_ld<NC>(sS, v);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float mul = kQ4 ? q_mul[(tc & 1) * N + c0 + c] : a.scale_log2;
-          const bool see = all || (some && t <= pos[c0 + c] && (a.window == 0 || t > pos[c0 + c] - a.window || t < s.snk));
-          v[c] = see ? v[c] * mul : -INFINITY;
-        }
-        bool over = b == s.b0;
+          for (int c = 0; c < NC; c += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(lm + c0 + c);
+            float4 y = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
+            if (kQ4) y = *reinterpret_cast<const float4*>(qm + c0 + c);
+            v[c] = less(v[c], y.x, x.x);
+            v[c + 1] = less(v[c + 1], y.y, x.y);
+            v[c + 2] = less(v[c + 2], y.z, x.z);
+            v[c + 3] = less(v[c + 3], y.w, x.w);
+          }
+          if (!plain) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) over = over || v[c] > mx[c0 + c] + kRescale;
-        if (named_any(bar_half, 128, over)) {
-          // the tokens' maximum of each row, then the running maximum, the sums and O^T move to it
+            for (int c = 0; c < NC; ++c) {
+              const int p = pos[c0 + c];
+              const bool see = all || (some && t <= p && (a.window == 0 || t > p - a.window || t < s.snk));
+              v[c] = see ? v[c] : -INFINITY;
+            }
+          }
+        };
+        scores(std::true_type{});
+        float top = v[0];
+#pragma unroll
+        for (int c = 1; c < NC; ++c) top = fmaxf(top, v[c]);
+        if (named_any(bar_half, 128, b == s.b0 || top > kRescale + C::kBias)) {
+          // the tokens' maximum of each row; then the running maximum, the sums and O^T move to it
+          tmem_ld<NC>(sS, v);
+          tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            const uint32_t w = __reduce_max_sync(kFull, order_bits(fmaxf(v[c], -INFINITY)));
-            if (lane == 0) warp_max[sw * NC + c] = unorder_bits(w);
+            const int p = pos[c0 + c];
+            const bool see = all || (some && t <= p && (a.window == 0 || t > p - a.window || t < s.snk));
+            const float x = see ? __fmul_rn(v[c], kQ4 ? qm[c0 + c] : a.scale_log2) : -INFINITY;
+            const uint32_t w = __reduce_max_sync(kFull, order_bits(fmaxf(x, -INFINITY)));  // NaN: -inf
+            if (lane == 0) warp_max[warp * NC + c] = unorder_bits(w);
           }
           named_sync(bar_half, 128);
-          float fac[NC];
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float* wm = warp_max + 4 * hw * NC + c;
-            const float old = mx[c0 + c];
+          if (quad == 0 && lane < NC) {
+            const float* wm = warp_max + 4 * hw * NC + lane;
+            const float old = C::kBias - lm[c0 + lane];
             const float now = fmaxf(old, fmaxf(fmaxf(wm[0], wm[NC]), fmaxf(wm[2 * NC], wm[3 * NC])));
-            fac[c] = ex2(old - now);
-            l[c] *= fac[c];
-            if (quad == 0 && lane == 0) warp_sum[4 * hw * NC + c] = now;  // free until the tile's end
+            lm[c0 + lane] = C::kBias - now;
+            move_by[c0 + lane] = ex2(old - now);
           }
           named_sync(bar_half, 128);
-          if (quad == 0 && lane < NC) mx[c0 + lane] = warp_sum[4 * hw * NC + lane];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) l[c] *= move_by[c0 + c];
           if (b > s.b0) {
             // s_full came after every earlier MMA, so O^T is at rest
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
-              float o[NC];
-              tmem_ld<NC>(tmem + lane_addr + (uint32_t)(i * N + c0), o);
-              tmem_wait_ld();
+#pragma unroll 1
+              for (int c = 0; c < NC; c += 8) {
+                float o[8];
+                tmem_ld8(tmem + lane_addr + (uint32_t)(i * N + c0 + c), o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < NC; ++c) o[c] *= fac[c];
-#pragma unroll
-              for (int c = 0; c < NC; c += 8) tmem_st8(tmem + lane_addr + (uint32_t)(i * N + c0 + c), o + c);
+                for (int k = 0; k < 8; ++k) o[k] *= move_by[c0 + c + k];
+                tmem_st8(tmem + lane_addr + (uint32_t)(i * N + c0 + c), o);
+              }
             }
             tmem_wait_st();
           }
-          named_sync(bar_half, 128);
+          scores(std::false_type{});
+          named_sync(bar_half, 128);  // move_by is free
         }
         // weights; the sum keeps them in fp32
         uint32_t p[NC / 2];
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {
-          const float e0 = ex2(v[c] - (mx[c0 + c] - C::kBias)), e1 = ex2(v[c + 1] - (mx[c0 + c + 1] - C::kBias));
+          const float e0 = ex2(v[c]), e1 = ex2(v[c + 1]);
           l[c] += e0;
           l[c + 1] += e1;
           if (kQ4) {
@@ -861,26 +899,29 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
           for (int c = 0; c < NC; ++c)
             st_u16(swz(slab, c0 + c, in >> 3) + (uint32_t)(in & 7) * 2u, (uint16_t)(p[c / 2] >> (16 * (c & 1))));
         }
-        // A row that some positions of the tile see and others do not: its weight is 0 for the others, and 0
-        // times what is not finite would reach them.  Its values that are not finite become 0 here; where it is
-        // seen its score is not finite either.
-        uint32_t edge = __ballot_sync(kFull, some);
-        while (edge) {
-          const int r = 32 * quad + __ffs(edge) - 1;
-          edge &= edge - 1u;
-          // this half's two pairs: 32 chunks of 8 elements
-          const int i = 2 * hw + (lane >> 4), slot = (4 * g + i) % C::kRing;
-          const uint32_t at = swz(sb + C::kRingOff + (uint32_t)slot * kPair + (uint32_t)((lane >> 3) & 1) * kSlab, r, lane & 7);
-          const uint4 x = ld_v4(at);
-          constexpr uint32_t kExp = kQ4 ? 0x7c00u : 0x7f80u;
-          uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          bool bad = false;
+        if (!plain) {
+          // A weight of 0 times a value that is not finite would be NaN: the value elements of rows that a position
+          // of the tile does not see (another position's, or what lies in an unread place) that are not finite
+          // become 0.  A position that does see such a row has a score that is not finite either.
+          uint32_t edge = __ballot_sync(kFull, !all);
+          const int i = 2 * hw + (lane >> 4), x4 = 4 * g + i;  // this half's two pairs: 32 chunks of 8 elements
+          if (!wait(&B.e_full[x4 % C::kRing], (uint32_t)(x4 / C::kRing))) { ok = false; break; }
+          const uint32_t slab = sb + C::kRingOff + (uint32_t)(x4 % C::kRing) * kPair + (uint32_t)((lane >> 3) & 1) * kSlab;
+          while (edge) {
+            const int r = 32 * quad + __ffs(edge) - 1;
+            edge &= edge - 1u;
+            const uint32_t at = swz(slab, r, lane & 7);
+            const uint4 x = ld_v4(at);
+            constexpr uint32_t kExp = kQ4 ? 0x7c00u : 0x7f80u;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            bool bad = false;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if ((w[e] & kExp) == kExp) { w[e] &= 0xffff0000u; bad = true; }
-            if ((w[e] & (kExp << 16)) == (kExp << 16)) { w[e] &= 0x0000ffffu; bad = true; }
+            for (int e = 0; e < 4; ++e) {
+              if ((w[e] & kExp) == kExp) { w[e] &= 0xffff0000u; bad = true; }
+              if ((w[e] & (kExp << 16)) == (kExp << 16)) { w[e] &= 0x0000ffffu; bad = true; }
+            }
+            if (bad) st_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
           }
-          if (bad) st_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
         }
         fence_proxy_async_smem();
         tc_before();
@@ -893,7 +934,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
         float x = l[c];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-        if (lane == 0) warp_sum[sw * NC + c] = x;
+        if (lane == 0) warp_sum[warp * NC + c] = x;
       }
       named_sync(bar_half, 128);
       if (quad == 0 && lane < NC) {
@@ -903,10 +944,10 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1) attend_paged_kerne
         row_inv[row] = sum == 0.f ? 0.f : 1.f / sum;
         if (s.part >= 0) {
           float* ml = a.part_ml + ((int64_t)blockIdx.x * 2 + s.part) * 2 * N;
-          ml[row] = mx[row];
+          ml[row] = C::kBias - lm[row];
           ml[N + row] = sum;
         } else if (a.lse && row < s.nrows) {
-          a.lse[s.grow + row] = sum == 0.f ? -INFINITY : (mx[row] - C::kBias + log2f(sum)) * 0.6931471805599453f;
+          a.lse[s.grow + row] = sum == 0.f ? -INFINITY : (log2f(sum) - lm[row]) * 0.6931471805599453f;
         }
       }
       named_sync(bar_half, 128);
@@ -1027,13 +1068,48 @@ __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArg
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's tensor-map encoder (the library is linked against the runtime alone).
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// [rows][576] bf16 in boxes of 64 elements x box_rows, 128-byte swizzled.
+bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
+  const EncodeTiled fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)kRow, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)kRowBytes16};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int N, bool kQ4>
 cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
   using C = Shape<N, kQ4>;
+  if (a.n_tokens == 0) return cudaMemsetAsync(a.status, 0, 4, s);
   cudaError_t e = cudaFuncSetAttribute(attend_paged_kernel<N, kQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
+  Maps maps{};
+  if (!kQ4) {
+    maps.run = a.B & -a.B;
+    if (maps.run > kBlk) maps.run = kBlk;
+    if (!encode_rows(&maps.pool, a.pool, a.n_blocks * a.B, maps.run) ||
+        !encode_rows(&maps.q, a.q, (int64_t)a.n_tokens * a.H, N))
+      return cudaErrorInvalidValue;
+  }
   schedule_paged_kernel<<<1, kSchedThreads, 0, s>>>(a, N);
-  attend_paged_kernel<N, kQ4><<<a.workers, C::kThreads, C::kSmem, s>>>(a);
+  attend_paged_kernel<N, kQ4><<<a.workers, C::kThreads, C::kSmem, s>>>(a, maps);
   join_paged_kernel<N><<<2 * a.workers, kJoinThreads, 0, s>>>(a, C::kBias);
   return cudaGetLastError();
 }
