@@ -57,7 +57,9 @@ def test_attend(L, over):
 
 
 def test_sizes(L):
-    assert L.kvo_paged_block_bytes(K.KVO_CACHE_BF16, 64) == 64 * 1152 and L.kvo_paged_block_bytes(K.KVO_CACHE_Q4, 64) == 64 * 324
+    for b in (8, 24, 64, 65536):
+        assert L.kvo_paged_block_bytes(K.KVO_CACHE_BF16, b) == K.kvo_paged_block_bytes(K.KVO_CACHE_BF16, b) == b * 1152
+        assert L.kvo_paged_block_bytes(K.KVO_CACHE_Q4, b) == K.kvo_paged_block_bytes(K.KVO_CACHE_Q4, b) == b * 324
     for fmt, b in ((2, 64), (0, 0), (0, 4), (1, 65544)):
         assert L.kvo_paged_block_bytes(fmt, b) == 0
     for r, t, h in ((0, 1, 16), (4097, 1, 16), (1, -1, 16), (1, 1, 0), (1, 1, 8193)):

@@ -16,6 +16,11 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
+// Every thread of the launch (one CTA, or a cluster).
+__device__ __forceinline__ void plan_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // First block that a position at or after length L can still see behind the
 // sinks' blocks: blocks [sb, dead_end(L)) are seen by none.
 __device__ __forceinline__ int dead_end(int L, int B, int window, int sb) {
@@ -25,29 +30,37 @@ __device__ __forceinline__ int dead_end(int L, int B, int window, int sb) {
 }
 
 // ---------------------------------------------------------------------------
-// plan: one CTA.  Each request's needs (new blocks, new tokens, blocks given
-// back) are prefix-summed over the requests, then the flat lists of new blocks,
-// released blocks and slots are filled by all threads, each entry finding its
-// request by a search in the prefix arrays (shared memory).
-// Latency is all it costs (a few KB read and written): one launch, and about
-// as many barriers as there are prefix sums.
+// plan: one CTA, or a cluster of kPlanCtas when there are many slots to write.
+// Each CTA reads the requests and prefix-sums their needs (new tokens, new
+// blocks, released blocks) for itself; after a barrier (outputs may be the
+// inputs) the flat lists of new blocks, slots and released blocks are shared
+// out over all threads, each entry finding its request by a search in the
+// prefix arrays (shared memory).  A few KB to a few hundred KB are moved, so
+// latency is all it costs.
 // ---------------------------------------------------------------------------
+constexpr int kPlanCtas = 8;
+constexpr int kPlanSlots = 4096;  // slots that one CTA writes alone
+
 __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs a) {
   extern __shared__ int32_t sm[];
   __shared__ int64_t warp_sums[33];
+  __shared__ int32_t taken;
   const int R = a.R, B = a.B;
   int32_t* cu = sm;              // [R + 1] new tokens before each request
-  int32_t* nb = cu + R + 1;      // [R + 1] new blocks before each request
-  int32_t* rel = nb + R + 1;     // [R + 1] released blocks before each request
+  int32_t* nb = cu + R + 1;      // [R] new blocks before each request
+  int32_t* rel = nb + R;         // [R + 1] released blocks before each request
   int32_t* old = rel + R + 1;    // [R] cached tokens; -1: refused
+  int32_t* ends = old + R;       // [R] 1: the request ends
+  const int tid = threadIdx.x, cta = blockIdx.x, step = kPlanThreads * gridDim.x;
   const int sb = (a.sinks + B - 1) / B;
   const int64_t head = a.ring_in[0], tail = a.ring_in[1];
   const int64_t F = a.ring_size;
   int64_t avail = tail - head;
   avail = avail < 0 || head < 0 ? 0 : (avail > F ? F : avail);
+  if (tid == 0) taken = 0;
   int64_t tok0 = 0, blk0 = 0, rel0 = 0;
   for (int base = 0; base < R; base += kPlanThreads) {
-    const int r = base + (int)threadIdx.x;
+    const int r = base + tid;
     int len = 0, n = 0, have = 0;
     int64_t grow = 0, need = 0;
     bool fits = true;
@@ -64,88 +77,87 @@ __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs 
       cu[r] = (int32_t)(c < INT32_MAX ? c : INT32_MAX);
       if (grow > 0 && c + grow > a.n_slots) fits = false;
       have = fits ? (len + B - 1) / B : 0;
-      need = fits ? (len + grow + B - 1) / B - have : 0;
+      need = fits ? (int)(len + grow + B - 1) / B - have : 0;
     }
-    const int64_t nb_at = block_exclusive_sum<kPlanThreads>(need, warp_sums, &total);
-    const bool served = fits && (need == 0 || blk0 + nb_at + need <= avail);
+    const int64_t nb_at = blk0 + block_exclusive_sum<kPlanThreads>(need, warp_sums, &total);
+    blk0 += total;
     // blocks are taken in request order: the served requests that need some are
     // a prefix of those, so what comes before a served one is served too
+    const bool served = fits && (need == 0 || nb_at + need <= avail);
     int64_t gone = 0;
     if (r < R) {
-      nb[r] = (int32_t)(blk0 + nb_at < avail ? blk0 + nb_at : avail);
+      nb[r] = (int32_t)(nb_at < avail ? nb_at : avail);
+      if (served && need > 0) atomicMax(&taken, (int32_t)(nb_at + need));
       if (served && n < 0) {
         gone = min(sb, have) + max(0, have - dead_end(len, B, a.window, sb));
       } else if (served) {
         const int hi = min(dead_end(len + (int)grow, B, a.window, sb), have + (int)need);
         gone = max(0, hi - dead_end(len, B, a.window, sb));
       }
+      old[r] = served ? len : fits ? -1 : -2;
+      ends[r] = n < 0 ? 1 : 0;
     }
-    blk0 += total;
     const int64_t rel_at = rel0 + block_exclusive_sum<kPlanThreads>(gone, warp_sums, &total);
     rel0 += total;
-    if (r < R) {
-      rel[r] = (int32_t)(rel_at < F ? rel_at : F);
-      const int after = n < 0 ? 0 : len + (int)grow;
-      old[r] = served ? len : -1;
-      a.lengths_out[r] = served ? after : len;
-      a.kv_lens[r] = served ? after : 0;
-      a.status[r] = served ? KVO_OK : (fits ? KVO_ECAPACITY : KVO_ERANGE);
-    }
-    // the next chunk's served requests start behind what this one took
-    if (blk0 > avail) blk0 = avail + 1;
+    if (r < R) rel[r] = (int32_t)(rel_at < F ? rel_at : F);
   }
-  __syncthreads();
-  // new blocks taken: the last served request's end
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     cu[R] = (int32_t)(tok0 < INT32_MAX ? tok0 : INT32_MAX);
     rel[R] = (int32_t)(rel0 < F ? rel0 : F);
   }
-  __syncthreads();
-  for (int r = threadIdx.x; r <= R; r += kPlanThreads) a.cu_new[r] = cu[r];
-  __shared__ int32_t taken;
-  if (threadIdx.x == 0) taken = 0;
-  __syncthreads();
-  for (int r = threadIdx.x; r < R; r += kPlanThreads) {
-    if (old[r] >= 0) {
-      const int grow = cu[r + 1] - cu[r];
-      const int need = (old[r] + grow + B - 1) / B - (old[r] + B - 1) / B;
-      if (need > 0) atomicMax(&taken, nb[r] + need);
-    }
-  }
-  __syncthreads();
+  plan_barrier();  // every input but the table and the ring has been read
   const int n_new = taken, n_rel = rel[R];
-  for (int i = threadIdx.x; i < n_new; i += kPlanThreads) {
-    // the last request that starts at or before entry i and needs blocks
-    const int r = segment_of(nb, R, i);
-    a.table[(int64_t)r * a.M + (old[r] + B - 1) / B + (i - nb[r])] = a.ring[(head + i) % F];
-  }
-  __syncthreads();  // tables complete; every taken entry read before the ring is written
-  for (int i = threadIdx.x; i < n_rel; i += kPlanThreads) {
-    const int r = segment_of(rel, R, i);
-    const int k = i - rel[r], len = old[r];
-    int j;
-    if (a.new_tokens[r] < 0) {
-      const int s = min(sb, (len + B - 1) / B);
-      j = k < s ? k : dead_end(len, B, a.window, sb) + (k - s);
+  const auto ring_at = [&](int64_t i) -> int64_t { return i < F ? i : i - F; };
+  const int64_t head0 = head < 0 ? 0 : head % F, tail0 = tail < 0 ? 0 : tail % F;
+  for (int r = cta * kPlanThreads + tid; r < R; r += step) {
+    const int len = old[r], grow = cu[r + 1] - cu[r];
+    a.cu_new[r] = cu[r];
+    if (len >= 0) {
+      const int after = ends[r] ? 0 : len + grow;
+      a.lengths_out[r] = after;
+      a.kv_lens[r] = after;
+      a.status[r] = KVO_OK;
     } else {
-      j = dead_end(len, B, a.window, sb) + k;
+      // a refused request keeps its length: in place already, unless the arrays differ
+      if (a.lengths_out != a.lengths) a.lengths_out[r] = a.lengths[r];
+      a.kv_lens[r] = 0;
+      a.status[r] = len == -1 ? KVO_ECAPACITY : KVO_ERANGE;
     }
-    a.ring[(tail + i) % F] = a.table[(int64_t)r * a.M + j];
   }
-  for (int i = threadIdx.x; i < a.n_slots; i += kPlanThreads) {
+  if (cta == 0 && tid == 0) {
+    a.cu_new[R] = cu[R];
+    a.ring_out[0] = head + n_new;
+    a.ring_out[1] = tail + n_rel;
+  }
+  for (int i = cta * kPlanThreads + tid; i < n_new; i += step) {
+    // the last request that starts at or before entry i (those of its place that need none come before it)
+    const int r = segment_of(nb, R, i);
+    a.table[(int64_t)r * a.M + (old[r] + B - 1) / B + (i - nb[r])] = a.ring[ring_at(head0 + i)];
+  }
+  for (int i = cta * kPlanThreads + tid; i < a.n_slots; i += step) {
     int32_t slot = -1;
     if (i < cu[R]) {
       const int r = segment_of(cu, R, i);
       if (old[r] >= 0) {
-        const int t = old[r] + (i - cu[r]);
-        slot = a.table[(int64_t)r * a.M + t / B] * B + t % B;
+        const int t = old[r] + (i - cu[r]), j = t / B, have = (old[r] + B - 1) / B;
+        // the request's last old block, or one of its new ones (another thread may not have written that entry yet)
+        const int32_t b = j < have ? a.table[(int64_t)r * a.M + j] : a.ring[ring_at(head0 + nb[r] + (j - have))];
+        slot = b * B + (t - j * B);
       }
     }
     a.slots[i] = slot;
   }
-  if (threadIdx.x == 0) {
-    a.ring_out[0] = head + n_new;
-    a.ring_out[1] = tail + n_rel;
+  if (n_rel == 0) return;
+  plan_barrier();  // tables complete, and every taken entry of the ring read
+  for (int i = cta * kPlanThreads + tid; i < n_rel; i += step) {
+    const int r = segment_of(rel, R, i);
+    const int k = i - rel[r], len = old[r];
+    int j = dead_end(len, B, a.window, sb) + k;
+    if (ends[r]) {
+      const int s = min(sb, (len + B - 1) / B);
+      j = k < s ? k : j - s;
+    }
+    a.ring[ring_at(tail0 + i)] = a.table[(int64_t)r * a.M + j];
   }
 }
 
@@ -289,13 +301,24 @@ int rows_call(PagedRowsArgs& a, const void* rows, const int32_t* slots, int64_t 
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s) {
-  const size_t smem = (4 * (size_t)a.R + 3) * 4;
+  const size_t smem = (5 * (size_t)a.R + 2) * 4;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(plan_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  plan_paged_kernel<<<1, kPlanThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  const unsigned ctas = a.n_slots > kPlanSlots ? kPlanCtas : 1;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ctas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(ctas);
+  c.blockDim = dim3(kPlanThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, plan_paged_kernel, a);
 }
 cudaError_t launch_paged_write(const PagedRowsArgs& a, bool q4, cudaStream_t s) {
   return q4 ? launch_rows(write_paged_kernel<true>, a, s) : launch_rows(write_paged_kernel<false>, a, s);

@@ -108,10 +108,11 @@ struct PagedAttendArgs {
   uint64_t wait_ns;
   int32_t workers;         // CTAs of the attention launch
   // workspace
-  int32_t* head;           // mode, tiles, workers in use
+  int32_t* head;           // listed, tiles, CTAs in use, shared tiles
   int32_t* tile_off;       // [R + 1] tiles before each request
   int4* tiles;             // [kListTiles] request, first row, blocks, cost before
   int2* start;             // [workers + 1] tile, unit
+  int4* shared;            // [workers] tile, first and last CTA, slot of the first one's part
   float* part_ml;          // [workers][2][2][N]
   float* part_o;           // [workers][2][N][512]
 };

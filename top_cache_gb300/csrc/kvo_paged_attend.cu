@@ -166,6 +166,10 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[NC]) {
 __device__ __forceinline__ uint32_t swz(uint32_t slab, int r, int c) {
   return slab + (uint32_t)r * 128u + ((uint32_t)(c ^ (r & 7)) << 4);
 }
+// The same box into L2 alone.
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
 // A box of a 2-D tensor map (x: element, y: row), completion counted in bytes on bar.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
@@ -201,6 +205,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// The next launch of the stream may start its set-up; grid_wait: the last one is done and its writes are visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- the work -------------------------------------------------------------------------------
 // One tile, or the part of its blocks that this CTA has.
@@ -251,7 +259,7 @@ __device__ __forceinline__ int request_rows(const PagedAttendArgs& a, int r) {
 }
 
 // Parts of the workspace header.
-constexpr int kHdListed = 0, kHdTiles = 1, kHdWorkers = 2;
+constexpr int kHdListed = 0, kHdTiles = 1, kHdWorkers = 2, kHdShared = 3;
 
 // The segments of one CTA, in order; every warp that walks them calls next()
 // with all lanes.
@@ -315,13 +323,19 @@ struct Walk {
 // the blocks before each, and where each CTA's even share starts.
 // ---------------------------------------------------------------------------
 constexpr int kSchedThreads = 1024;
+static_assert(kListTiles == 2 * kSchedThreads, "two tiles a thread");
 
 __global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAttendArgs a, int N) {
   __shared__ int64_t warp_sums[33];
-  __shared__ int32_t off[kMaxRequests + 1];
+  __shared__ int32_t off[kMaxRequests + 1];      // tiles before each request
+  __shared__ int32_t before[kListTiles];         // units before each tile
+  __shared__ int32_t n_shared;
+  launch_dependents();
+  const int tid = threadIdx.x;
   int64_t total = 0, sum;
+  if (tid == 0) n_shared = 0;
   for (int base = 0; base < a.R; base += kSchedThreads) {
-    const int r = base + (int)threadIdx.x;
+    const int r = base + tid;
     const int64_t n = r < a.R ? (request_rows(a, r) + N - 1) / N : 0;
     const int64_t at = total + block_exclusive_sum<kSchedThreads>(n, warp_sums, &sum);
     if (r < a.R) a.tile_off[r] = off[r] = (int32_t)at;
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAtte
   }
   const int n_tiles = (int)total;
   const bool listed = n_tiles <= kListTiles;
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     a.tile_off[a.R] = n_tiles;
     a.head[kHdListed] = listed ? 1 : 0;
     a.head[kHdTiles] = n_tiles;
@@ -339,40 +353,46 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAtte
   if (!listed) return;
   // thread i lists tiles 2 i and 2 i + 1
   int cost[2] = {0, 0};
-  int4 d[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int i = 2 * (int)threadIdx.x + k;
+    const int i = 2 * tid + k;
     if (i < n_tiles) {
       const int r = segment_of(off, a.R, i);
       Seg s;
       tile_of(a, N, r, (i - off[r]) * N, s);
       cost[k] = s.nblk + kTileCost;
-      d[k] = make_int4(r, s.row0, s.nblk, 0);
+      a.tiles[i] = make_int4(r, s.row0, s.nblk, 0);
     }
   }
+  // at most 2048 tiles of at most 2^23 + 1 units: the sum can pass 2^31, and is then cut off (the shares only get uneven)
   int64_t units;
-  int64_t at = block_exclusive_sum<kSchedThreads>((int64_t)cost[0] + cost[1], warp_sums, &units);
+  const int64_t at0 = block_exclusive_sum<kSchedThreads>((int64_t)cost[0] + cost[1], warp_sums, &units);
+  before[2 * tid] = (int32_t)min(at0, (int64_t)INT32_MAX);
+  before[2 * tid + 1] = (int32_t)min(at0 + cost[0], (int64_t)INT32_MAX);
   const int64_t share = max((int64_t)kMinShare, (units + a.workers - 1) / a.workers);
   const int used = (int)min((int64_t)a.workers, (units + share - 1) / share);
+  __syncthreads();
+  // CTA w starts at unit w * units / used
+  for (int w = tid; w < used; w += kSchedThreads) {
+    const int64_t u = (int64_t)w * units / used;
+    const int i = segment_of(before, n_tiles, (int)min(u, (int64_t)INT32_MAX));
+    a.start[w] = make_int2(i, (int)(u - before[i]));
+  }
+  // the CTAs of a tile's first and last block; the first one's part lies in slot 1 if it also has the tile's own unit
+  int64_t at = at0;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int i = 2 * (int)threadIdx.x + k;
-    if (i < n_tiles) {
-      d[k].w = (int)min(at, (int64_t)INT32_MAX);
-      a.tiles[i] = d[k];
-      // CTA w starts at unit w * units / used
-      for (int64_t w = (at * used + units - 1) / units; w < used; ++w) {
-        const int64_t u = w * units / used;
-        if (u >= at + cost[k]) break;
-        if (u >= at) a.start[w] = make_int2(i, (int)(u - at));
-      }
-      at += cost[k];
+    if (cost[k] > kTileCost) {
+      const int w0 = (int)(((at + kTileCost + 1) * used - 1) / units), w1 = (int)(((at + cost[k]) * used - 1) / units);
+      if (w1 > w0) a.shared[atomicAdd(&n_shared, 1)] = make_int4(2 * tid + k, w0, w1, (int64_t)w0 * units / used <= at ? 1 : 0);
     }
+    at += cost[k];
   }
-  if (threadIdx.x == 0) {
+  __syncthreads();
+  if (tid == 0) {
     a.start[used] = make_int2(n_tiles, 0);
     a.head[kHdWorkers] = used;
+    a.head[kHdShared] = n_shared;
   }
 }
 
@@ -383,6 +403,7 @@ struct Bars {
   uint64_t q_full, q_free, r_full, r_free, s_full, p_full, o_done, o_free, fin;
   uint64_t e_full[kMaxRing], e_free[kMaxRing];
   uint32_t tmem, abort;
+  uint32_t dead[2][2];  // softmax: a warp of the half gave up, by parity of the barrier's count
 };
 static_assert(sizeof(Bars) <= 256, "barriers");
 
@@ -463,7 +484,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
   };
   if (tid == 0) {
     mbar_init(&B.q_full, C::kFillers);
-    mbar_init(&B.q_free, 1);
+    mbar_init(&B.q_free, kQ4 ? 3 : 1);  // the last S^T done; 4 bits: and both softmax halves have seen the factors in place
     mbar_init(&B.r_full, C::kFillers);
     mbar_init(&B.r_free, 1);
     mbar_init(&B.s_full, 1);
@@ -476,6 +497,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       mbar_init(&B.e_free[i], 1);
     }
     B.abort = 0u;
+    B.dead[0][0] = B.dead[0][1] = B.dead[1][0] = B.dead[1][1] = 0u;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -493,6 +515,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
     return __all_sync(kFull, mbar_wait(bar, parity & 1u, a.wait_ns)) && !__any_sync(kFull, *abort_flag != 0u);
   };
 
+  grid_wait();
   Walk<N> walk;
   walk.begin(a);
   Seg s;
@@ -523,7 +546,15 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         int next = find(s.b0);
         for (int b = s.b0; b < s.b1; ++b, ++g) {
           const int row = next;
-          if (b + 1 < s.b1) next = find(b + 1);
+          if (b + 1 < s.b1) {
+            // a block ahead into L2: the ring has room for little more than one block
+            next = find(b + 1);
+            if (next >= 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) tma_prefetch(&maps.pool, 128 * i + 64 * (lane & 1), next);
+              if (!(lane & 1)) tma_prefetch(&maps.pool, kVal, next);
+            }
+          }
           const uint32_t got = __popc(__ballot_sync(kFull, row >= 0)) >> 1;  // runs
           const uint32_t off = (uint32_t)((lane >> 1) * run) * 128u;
 #pragma unroll
@@ -761,8 +792,20 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
     const int c0 = hw * NC;                               // its first row of the tile
     const uint32_t lane_addr = (uint32_t)(32 * quad) << 16;
     const uint32_t sS = tmem + lane_addr + C::kColS + (uint32_t)c0;
-    const uint32_t bar_half = 2u + (uint32_t)hw;          // 128 threads with the same rows
-    bool ok = true;
+    const uint32_t bar_half = 1u + (uint32_t)hw;          // 128 threads with the same rows
+    // A warp whose wait expires still meets the others of its half at their next barrier and tells them there, so
+    // that all four leave together: the flag of a barrier is set before it and read after it, and no warp can be two
+    // barriers that carry one ahead of another.
+    int meets = 0;
+    bool dead = false;
+    auto meet = [&](bool vote, bool& any) -> bool {  // false: leave
+      volatile uint32_t* f = &B.dead[meets & 1][hw];
+      ++meets;
+      if (dead) *f = 1u;
+      any = named_any(bar_half, 128, vote);
+      return *f == 0u;
+    };
+    bool ok = true, any;
     while (ok && walk.next(a, s)) {
       if (s.b0 >= s.b1) {  // nothing visible
         for (int i = st; i < s.nrows * (kVal / 8); i += kSoftThreads)
@@ -773,12 +816,15 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       float* lm = less_max + (tc & 1) * N;
       int32_t* pos = row_pos + (tc & 1) * N;
       const float* qm = q_mul + (tc & 1) * N;
-      if (st < N) {
-        lm[st] = C::kBias - kNone;
-        pos[st] = s.pos0 + (s.row0 + min(st, s.nrows - 1)) / s.H;
+      if (quad == 0 && lane < NC) {
+        lm[c0 + lane] = C::kBias - kNone;
+        pos[c0 + lane] = s.pos0 + (s.row0 + min(c0 + lane, s.nrows - 1)) / s.H;
       }
-      if (kQ4 && !wait(&B.q_full, (uint32_t)tc)) { ok = false; break; }  // the factors
-      named_sync(1, kSoftThreads);
+      if (kQ4) {  // the factors; the next tile's queries may not be announced before both halves have seen these
+        dead = dead || !wait(&B.q_full, (uint32_t)tc);
+      }
+      if (!meet(false, any)) { ok = false; break; }
+      if (kQ4 && quad == 0 && lane == 0) mbar_arrive(&B.q_free);
       const int32_t* table = a.table + (int64_t)s.r * a.M;
       float l[NC];
 #pragma unroll
@@ -794,20 +840,35 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         const int t = s.block(b) * kBlk + tok;
         // the token is seen by every position of the tile, or by some
         const bool all = here && t <= s.pmin && (a.window == 0 || t > s.pmax - a.window || t < s.snk);
-        const bool some = here && !all;
         const bool plain = __all_sync(kFull, all);
-        if (!wait(&B.s_full, (uint32_t)g)) { ok = false; break; }
+        // bit c: row c0 + c sees the token.  Position p sees token t when p - t is in [0, span).
+        uint32_t vis = kFull;
+        if (!plain) {
+          const uint32_t span = !here ? 0u : (a.window == 0 || t < s.snk) ? 0x7fffffffu : (uint32_t)a.window;
+          vis = 0u;
+#pragma unroll
+          for (int c = 0; c < NC; c += 4) {
+            const int4 p = *reinterpret_cast<const int4*>(pos + c0 + c);
+            vis |= (uint32_t)((uint32_t)(p.x - t) < span) << c;
+            vis |= (uint32_t)((uint32_t)(p.y - t) < span) << (c + 1);
+            vis |= (uint32_t)((uint32_t)(p.z - t) < span) << (c + 2);
+            vis |= (uint32_t)((uint32_t)(p.w - t) < span) << (c + 3);
+          }
+        }
+        dead = dead || !wait(&B.s_full, (uint32_t)g);
         tc_after();
         float v[NC];
         // v: scores in log2 units less the running maximum (plus kBias); -inf where hidden.  Where the maximum has
         // just moved the product is rounded as the maximum was, so that its own score is no less than 0 however
         // large it is; else the two are fused.
+        bool odd = false;  // the token's raw scores are not finite: so is, or may be, its row
         auto scores = [&](auto fused) {
           auto less = [&](float x, float m, float y) {
             return decltype(fused)::value ? fmaf(x, m, y) : __fadd_rn(__fmul_rn(x, m), y);
           };
           tmem_ld<NC>(sS, v);
           tmem_wait_ld();
+          odd = !(fabsf(v[0]) < INFINITY);
 #pragma unroll
           for (int c = 0; c < NC; c += 4) {
             const float4 x = *reinterpret_cast<const float4*>(lm + c0 + c);
@@ -820,26 +881,21 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           }
           if (!plain) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const int p = pos[c0 + c];
-              const bool see = all || (some && t <= p && (a.window == 0 || t > p - a.window || t < s.snk));
-              v[c] = see ? v[c] : -INFINITY;
-            }
+            for (int c = 0; c < NC; ++c) v[c] = (vis >> c) & 1u ? v[c] : -INFINITY;
           }
         };
         scores(std::true_type{});
         float top = v[0];
 #pragma unroll
         for (int c = 1; c < NC; ++c) top = fmaxf(top, v[c]);
-        if (named_any(bar_half, 128, b == s.b0 || top > kRescale + C::kBias)) {
+        if (!meet(b == s.b0 || top > kRescale + C::kBias, any)) { ok = false; break; }
+        if (any) {
           // the tokens' maximum of each row; then the running maximum, the sums and O^T move to it
           tmem_ld<NC>(sS, v);
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            const int p = pos[c0 + c];
-            const bool see = all || (some && t <= p && (a.window == 0 || t > p - a.window || t < s.snk));
-            const float x = see ? __fmul_rn(v[c], kQ4 ? qm[c0 + c] : a.scale_log2) : -INFINITY;
+            const float x = (vis >> c) & 1u ? __fmul_rn(v[c], kQ4 ? qm[c0 + c] : a.scale_log2) : -INFINITY;
             const uint32_t w = __reduce_max_sync(kFull, order_bits(fmaxf(x, -INFINITY)));  // NaN: -inf
             if (lane == 0) warp_max[warp * NC + c] = unorder_bits(w);
           }
@@ -902,10 +958,11 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         if (!plain) {
           // A weight of 0 times a value that is not finite would be NaN: the value elements of rows that a position
           // of the tile does not see (another position's, or what lies in an unread place) that are not finite
-          // become 0.  A position that does see such a row has a score that is not finite either.
-          uint32_t edge = __ballot_sync(kFull, !all);
+          // become 0.  A row with such an element has no finite score (0 times infinity is NaN, and nothing finite
+          // comes of either), so the score of any one query tells, and a position that sees the row is not misled.
+          uint32_t edge = __ballot_sync(kFull, !all && odd);
           const int i = 2 * hw + (lane >> 4), x4 = 4 * g + i;  // this half's two pairs: 32 chunks of 8 elements
-          if (!wait(&B.e_full[x4 % C::kRing], (uint32_t)(x4 / C::kRing))) { ok = false; break; }
+          if (!mbar_wait(&B.e_full[x4 % C::kRing], (uint32_t)(x4 / C::kRing) & 1u, a.wait_ns)) fail();  // (S^T has read it)
           const uint32_t slab = sb + C::kRingOff + (uint32_t)(x4 % C::kRing) * kPair + (uint32_t)((lane >> 3) & 1) * kSlab;
           while (edge) {
             const int r = 32 * quad + __ffs(edge) - 1;
@@ -951,10 +1008,10 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         }
       }
       named_sync(bar_half, 128);
-      if (!wait(&B.o_done, (uint32_t)tc)) { ok = false; break; }
+      dead = dead || !wait(&B.o_done, (uint32_t)tc);
       tc_after();
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4 && !dead; ++i) {
         float o[NC];
         tmem_ld<NC>(tmem + lane_addr + (uint32_t)(i * N + c0), o);
         tmem_wait_ld();
@@ -982,10 +1039,11 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       mbar_arrive(&B.o_free);
       ++tc;
     }
-    if (!ok) fail();
+    if (!ok || dead) fail();
   }
   tc_before();
   __syncthreads();
+  launch_dependents();
   if (warp == kMmaWarp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
@@ -993,77 +1051,46 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// join: one CTA per (tile, row) of a tile that several CTAs share; warp w takes
-// 128 value elements and every fourth part, and the four sums meet in shared
-// memory in a fixed order.
+// join: the parts of a tile that several CTAs share, in CTA order.  128 threads
+// a row, four value elements each, several parts in flight.
 // ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 512;
+constexpr int kJoinRows = 4;  // rows per CTA
+constexpr int kJoinThreads = kJoinRows * kVal / 4;
 
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArgs a, float bias) {
+  grid_wait();
   if (a.head[kHdListed] == 0) return;
-  __shared__ float4 acc[3][128];
-  __shared__ float wsum[4];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int quarter = warp & 3, grp = warp >> 2;
-  const int used = a.head[kHdWorkers], n_tiles = a.head[kHdTiles];
-  // CTAs whose share starts inside a tile continue it: tile start[w].x is shared
-  // by the CTAs from the one before the first such w to the last
-  for (int item = blockIdx.x; item < used * N; item += gridDim.x) {
-    const int w0 = item / N, row = item - w0 * N;
-    // this item stands for the tile that CTA w0 leaves unfinished and begins (or is first to have blocks of)
-    if (w0 + 1 >= used) continue;
-    const int2 nx = a.start[w0 + 1];
-    if (nx.y <= kTileCost) continue;  // the next CTA starts a tile, or has all of its blocks
-    const int tile = nx.x;
-    const int2 me = a.start[w0];
-    // w0 is the tile's first CTA with blocks: its share starts before the tile's second block unit
-    if (!(me.x < tile || (me.x == tile && me.y <= kTileCost))) continue;
-    if (tile >= n_tiles) continue;
-    const int4 d = a.tiles[tile];
-    Seg s;
-    tile_of(a, N, d.x, d.y, s);
-    if (row >= s.nrows) continue;
-    int w1 = w0 + 1;  // last CTA with blocks of it
-    while (w1 + 1 < used && a.start[w1 + 1].x == tile) ++w1;
-    // w0's part: slot 1 when its share has the tile's own unit, else 0 (and so for every later one)
-    const int slot0 = me.x < tile || me.y < kTileCost ? 1 : 0;
-    float m = kNone;
-    for (int w = w0; w <= w1; ++w) m = fmaxf(m, a.part_ml[((int64_t)w * 2 + (w == w0 ? slot0 : 0)) * 2 * N + row]);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int w = w0 + grp; w <= w1; w += 4) {
-      const int64_t p = (int64_t)w * 2 + (w == w0 ? slot0 : 0);
-      const float f = ex2(a.part_ml[p * 2 * N + row] - m);
-      l += f * a.part_ml[p * 2 * N + N + row];
-      const float4 y = reinterpret_cast<const float4*>(a.part_o + (p * N + row) * kVal)[quarter * 32 + lane];
-      x.x += f * y.x;
-      x.y += f * y.y;
-      x.z += f * y.z;
-      x.w += f * y.w;
-    }
-    __syncthreads();
-    if (grp > 0) acc[grp - 1][quarter * 32 + lane] = x;
-    if (lane == 0 && quarter == 0) wsum[grp] = l;
-    __syncthreads();
-    if (grp == 0) {
-      const float L = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float4 y = acc[k][quarter * 32 + lane];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
-      }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
-      const __nv_bfloat162 h0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), h1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-      reinterpret_cast<uint2*>(a.out + (s.grow + row) * kVal)[quarter * 32 + lane] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-      if (tid == 0 && a.lse) a.lse[s.grow + row] = L == 0.f ? -INFINITY : (m - bias + log2f(L)) * 0.6931471805599453f;
-    }
+  const int item = (int)blockIdx.x * kJoinRows + (int)threadIdx.x / (kVal / 4), col = threadIdx.x % (kVal / 4);
+  const int row = item % N;
+  if (item / N >= a.head[kHdShared]) return;
+  const int4 sh = a.shared[item / N];  // tile, first CTA, last CTA, slot of the first one's part (0 for the others)
+  const int4 d = a.tiles[sh.x];
+  Seg s;
+  tile_of(a, N, d.x, d.y, s);
+  if (row >= s.nrows) return;
+  auto part = [&](int w) -> int64_t { return (int64_t)w * 2 + (w == sh.y ? sh.w : 0); };
+  float m = kNone;
+#pragma unroll 8
+  for (int w = sh.y; w <= sh.z; ++w) m = fmaxf(m, a.part_ml[part(w) * 2 * N + row]);
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 8
+  for (int w = sh.y; w <= sh.z; ++w) {
+    const int64_t p = part(w);
+    const float4 y = reinterpret_cast<const float4*>(a.part_o + (p * N + row) * kVal)[col];
+    const float f = ex2(a.part_ml[p * 2 * N + row] - m);
+    l += f * a.part_ml[p * 2 * N + N + row];
+    x.x += f * y.x;
+    x.y += f * y.y;
+    x.z += f * y.z;
+    x.w += f * y.w;
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const __nv_bfloat162 h0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), h1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+  reinterpret_cast<uint2*>(a.out + (s.grow + row) * kVal)[col] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+  if (col == 0 && a.lse) a.lse[s.grow + row] = l == 0.f ? -INFINITY : (m - bias + log2f(l)) * 0.6931471805599453f;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1094,6 +1121,22 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch whose set-up may overlap the last one's end (it calls grid_wait before it reads anything).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 template <int N, bool kQ4>
 cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
   using C = Shape<N, kQ4>;
@@ -1109,9 +1152,10 @@ cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
       return cudaErrorInvalidValue;
   }
   schedule_paged_kernel<<<1, kSchedThreads, 0, s>>>(a, N);
-  attend_paged_kernel<N, kQ4><<<a.workers, C::kThreads, C::kSmem, s>>>(a, maps);
-  join_paged_kernel<N><<<2 * a.workers, kJoinThreads, 0, s>>>(a, C::kBias);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_after(attend_paged_kernel<N, kQ4>, a.workers, C::kThreads, C::kSmem, s, a, maps);
+  if (e == cudaSuccess) e = launch_after(join_paged_kernel<N>, a.workers * N / kJoinRows, kJoinThreads, 0, s, a, C::kBias);
+  return e;
 }
 
 }  // namespace
@@ -1124,7 +1168,7 @@ int paged_tile_rows(int n_requests, int n_tokens, int H) {
 size_t paged_attend_workspace(int n_requests, int n_tokens, int H, int workers) {
   const size_t N = (size_t)paged_tile_rows(n_requests, n_tokens, H), W = (size_t)workers;
   return 256 + up256(((size_t)n_requests + 1) * 4) + up256(kListTiles * sizeof(int4)) + up256((W + 1) * sizeof(int2)) +
-         up256(W * 4 * N * 4) + W * 2 * N * kVal * 4;
+         up256(W * sizeof(int4)) +          up256(W * 4 * N * 4) + W * 2 * N * kVal * 4;
 }
 void paged_attend_carve(PagedAttendArgs& a, uint8_t* w) {
   const size_t N = (size_t)paged_tile_rows(a.R, a.n_tokens, a.H), W = (size_t)a.workers;
@@ -1137,6 +1181,8 @@ void paged_attend_carve(PagedAttendArgs& a, uint8_t* w) {
   w += up256(kListTiles * sizeof(int4));
   a.start = reinterpret_cast<int2*>(w);
   w += up256((W + 1) * sizeof(int2));
+  a.shared = reinterpret_cast<int4*>(w);
+  w += up256(W * sizeof(int4));
   a.part_ml = reinterpret_cast<float*>(w);
   w += up256(W * 4 * N * 4);
   a.part_o = reinterpret_cast<float*>(w);

@@ -338,54 +338,79 @@ def kvo_export_state(h, unit, max_tokens, capacity, row_elems=576, with_rows=Fal
             "stamp": sp.value, "hot": hot}
 
 
-def _tensor(t, name, dtype, device, shape=None):
-    """Address of a dense device tensor of the given type; shape entries of None are free."""
+_torch = None
+_types16 = ()  # bf16 rows, as themselves or as int16 bits (as elsewhere in this binding)
+
+
+def _with_torch():
+    global _torch, _types16
     import torch
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    _types16 = (torch.bfloat16, torch.int16)
+    _torch = torch
+    return torch
+
+
+def _dev(t, name, dtype, device, shape):
+    """Address of a dense tensor of the given type and shape on CUDA device `device` (an index)."""
+    try:
+        if (t.dtype is dtype or (dtype is _types16 and t.dtype in dtype)) and t.get_device() == device and t.shape == shape \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise KvoError(KVO_EINVAL, "%s must be a CUDA tensor" % name)
-    if device is not None and t.device != device:
-        raise KvoError(KVO_EINVAL, "%s is on %s, not on %s" % (name, t.device, device))
-    if (t.dtype is not dtype) if not isinstance(dtype, tuple) else (t.dtype not in dtype):
-        raise KvoError(KVO_EINVAL, "%s has type %s" % (name, t.dtype))
-    if shape is not None:
-        have = t.shape
-        if len(have) != len(shape) or any(n is not None and n != m for n, m in zip(shape, have)):
-            raise KvoError(KVO_EINVAL, "%s has shape %s, not %s" % (name, tuple(have), shape))
+    if t.get_device() != device:
+        raise KvoError(KVO_EINVAL, "%s is on %s, not on cuda:%d" % (name, t.device, device))
+    if t.shape != shape:
+        raise KvoError(KVO_EINVAL, "%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         raise KvoError(KVO_EINVAL, "%s is not contiguous" % name)
-    return t.data_ptr()
+    raise KvoError(KVO_EINVAL, "%s has type %s" % (name, t.dtype))
 
 
-def _on(device, stream, call):
-    """call(stream handle) with `device` current (the launches go there)."""
-    import torch
-    if device.index == torch.cuda.current_device():
-        return _check(call(_stream(stream)))
-    with torch.cuda.device(device):
-        return _check(call(_stream(stream)))
+def _sizes(t, name, dims):
+    """The shape of a CUDA tensor of that many dimensions, and its device's index."""
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
+        raise KvoError(KVO_EINVAL, "%s must be a CUDA tensor" % name)
+    if t.dim() != dims:
+        raise KvoError(KVO_EINVAL, "%s has %d dimensions, not %d" % (name, t.dim(), dims))
+    return t.shape, t.get_device()
 
 
-def _types16():
-    import torch
-    return (torch.bfloat16, torch.int16)  # int16: bf16 bits, as elsewhere in this binding
+def _launch(f, args, device, stream):
+    """f(*args, stream handle) with `device` current (the launches go there)."""
+    T = _torch._C
+    if stream is None:
+        s = T._cuda_getCurrentRawStream(device)
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if T._cuda_getDevice() == device:
+        rc = f(*args, s)
+    else:
+        with _torch.cuda.device(device):
+            rc = f(*args, s)
+    if rc != KVO_OK:
+        _check(rc)
 
 
 def _pool(pool, n_blocks, block_tokens, format):
     """Address and device of a cache's pool, whose bytes must hold n_blocks blocks."""
-    import torch
+    if not isinstance(pool, _torch.Tensor) or not pool.is_cuda:
+        raise KvoError(KVO_EINVAL, "pool must be a CUDA tensor")
     size = kvo_paged_block_bytes(format, block_tokens)
-    p = _tensor(pool, "pool", (torch.uint8, torch.bfloat16, torch.int16), None)
     if pool.numel() * pool.element_size() < n_blocks * size:
         raise KvoError(KVO_EINVAL, "pool is smaller than n_blocks blocks")
-    return p, pool.device
+    if not pool.is_contiguous():
+        raise KvoError(KVO_EINVAL, "pool is not contiguous")
+    return pool.data_ptr(), pool.get_device()
 
 
 def kvo_paged_block_bytes(format, block_tokens):
     """Bytes of one block of a paged device cache (KVO_CACHE_BF16 or KVO_CACHE_Q4)."""
-    n = int(lib().kvo_paged_block_bytes(format, block_tokens))
-    if n == 0:
-        raise KvoError(KVO_EINVAL, "unknown cache format, or block_tokens not a multiple of 8 in 8 .. 65536")
-    return n
+    if format in (KVO_CACHE_BF16, KVO_CACHE_Q4) and 8 <= block_tokens <= 65536 and block_tokens % 8 == 0:
+        return block_tokens * (1152 if format == KVO_CACHE_BF16 else 324)
+    raise KvoError(KVO_EINVAL, "unknown cache format, or block_tokens not a multiple of 8 in 8 .. 65536")
 
 
 def kvo_paged_plan(lengths, new_tokens, block_tokens, block_table, ring, ring_in, ring_out, lengths_out, kv_lens,
@@ -395,45 +420,36 @@ def kvo_paged_plan(lengths, new_tokens, block_tokens, block_table, ring, ring_in
     int32 CUDA tensors: lengths, new_tokens, lengths_out, kv_lens, status [R], block_table [R][max_blocks],
     ring [ring_size], cu_new [R + 1], slots [n_slots]; int64 [2]: ring_in, ring_out.
     """
-    import torch
-    i32, i64 = torch.int32, torch.int64
-    a = _tensor(lengths, "lengths", i32, None, (None,))
-    dev, R = lengths.device, lengths.shape[0]
-    one = (R,)
-    b = _tensor(new_tokens, "new_tokens", i32, dev, one)
-    t = _tensor(block_table, "block_table", i32, dev, (R, None))
-    f = _tensor(ring, "ring", i32, dev, (None,))
-    fi = _tensor(ring_in, "ring_in", i64, dev, (2,))
-    fo = _tensor(ring_out, "ring_out", i64, dev, (2,))
-    lo = _tensor(lengths_out, "lengths_out", i32, dev, one)
-    kv = _tensor(kv_lens, "kv_lens", i32, dev, one)
-    cu = _tensor(cu_new, "cu_new", i32, dev, (R + 1,))
-    sl = _tensor(slots, "slots", i32, dev, (None,))
-    st = _tensor(status, "status", i32, dev, one)
-    M, F, S = block_table.shape[1], ring.shape[0], slots.shape[0]
-    f_ = lib().kvo_paged_plan
-    return _on(dev, stream, lambda s: f_(a, b, R, block_tokens, M, window, sinks, t, f, F, fi, fo, lo, kv, cu, sl, S,
-                                         st, s))
+    t = _torch or _with_torch()
+    i32, i64 = t.int32, t.int64
+    one, d = _sizes(lengths, "lengths", 1)
+    (rows, M), F, S = _sizes(block_table, "block_table", 2)[0], _sizes(ring, "ring", 1)[0], _sizes(slots, "slots", 1)[0]
+    R = one[0]
+    _launch(lib().kvo_paged_plan, (
+        _dev(lengths, "lengths", i32, d, one), _dev(new_tokens, "new_tokens", i32, d, one), R, block_tokens, M, window,
+        sinks, _dev(block_table, "block_table", i32, d, (R, M)), _dev(ring, "ring", i32, d, F), F[0],
+        _dev(ring_in, "ring_in", i64, d, (2,)), _dev(ring_out, "ring_out", i64, d, (2,)),
+        _dev(lengths_out, "lengths_out", i32, d, one), _dev(kv_lens, "kv_lens", i32, d, one),
+        _dev(cu_new, "cu_new", i32, d, (R + 1,)), _dev(slots, "slots", i32, d, S), S[0],
+        _dev(status, "status", i32, d, one)), d, stream)
 
 
 def kvo_paged_write(rows, slots, pool, n_blocks, block_tokens, format, stream=None):
     """Rows (bf16 [n][576]) into the cache at slots (int32 [n], below 0: skipped)."""
-    import torch
-    p, dev = _pool(pool, n_blocks, block_tokens, format)
-    r = _tensor(rows, "rows", _types16(), dev, (None, 576))
-    n = rows.shape[0]
-    s = _tensor(slots, "slots", torch.int32, dev, (n,))
-    return _on(dev, stream, lambda st: lib().kvo_paged_write(r, s, n, p, n_blocks, block_tokens, format, st))
+    t = _torch or _with_torch()
+    p, d = _pool(pool, n_blocks, block_tokens, format)
+    n = _sizes(slots, "slots", 1)[0][0]
+    _launch(lib().kvo_paged_write, (_dev(rows, "rows", _types16, d, (n, 576)), _dev(slots, "slots", t.int32, d, (n,)), n,
+                                    p, n_blocks, block_tokens, format), d, stream)
 
 
 def kvo_paged_read(pool, n_blocks, block_tokens, format, slots, rows, stream=None):
     """The cache's values at slots (int32 [n]) into rows (bf16 [n][576]); skipped rows stay as they were."""
-    import torch
-    p, dev = _pool(pool, n_blocks, block_tokens, format)
-    r = _tensor(rows, "rows", _types16(), dev, (None, 576))
-    n = rows.shape[0]
-    s = _tensor(slots, "slots", torch.int32, dev, (n,))
-    return _on(dev, stream, lambda st: lib().kvo_paged_read(p, n_blocks, block_tokens, format, s, n, r, st))
+    t = _torch or _with_torch()
+    p, d = _pool(pool, n_blocks, block_tokens, format)
+    n = _sizes(slots, "slots", 1)[0][0]
+    _launch(lib().kvo_paged_read, (p, n_blocks, block_tokens, format, _dev(slots, "slots", t.int32, d, (n,)), n,
+                                   _dev(rows, "rows", _types16, d, (n, 576))), d, stream)
 
 
 _attend_sizes = {}
@@ -460,33 +476,29 @@ def kvo_paged_attend(pool, n_blocks, block_tokens, format, block_table, kv_lens,
     workspace: uint8 CUDA tensor of kvo_paged_attend_workspace_size bytes; by default one is taken from the
     caching allocator on the stream of the call.
     """
-    import torch
-    p, dev = _pool(pool, n_blocks, block_tokens, format)
-    i32 = torch.int32
-    kv = _tensor(kv_lens, "kv_lens", i32, dev, (None,))
-    R = kv_lens.shape[0]
-    t = _tensor(block_table, "block_table", i32, dev, (R, None))
-    cu = _tensor(cu_tokens, "cu_tokens", i32, dev, (R + 1,))
-    q = _tensor(queries, "queries", _types16(), dev, (None, None, 576))
-    T, H = queries.shape[0], queries.shape[1]
-    o = _tensor(out, "out", _types16(), dev, (T, H, 512))
-    e = None if lse is None else _tensor(lse, "lse", torch.float32, dev, (T, H))
-    st = None if status is None else _tensor(status, "status", (i32, torch.uint32), dev, (1,))
-    size = kvo_paged_attend_workspace_size(R, T, H, dev.index)
+    t = _torch or _with_torch()
+    i32 = t.int32
+    p, d = _pool(pool, n_blocks, block_tokens, format)
+    (T, H, _), (R, M) = _sizes(queries, "queries", 3)[0], _sizes(block_table, "block_table", 2)[0]
     if workspace is None:
-        if stream is not None and _stream(stream) != torch.cuda.current_stream(dev).cuda_stream:
+        size = kvo_paged_attend_workspace_size(R, T, H, d)
+        if stream is None or _stream(stream) == t._C._cuda_getCurrentRawStream(d):
+            workspace = t.empty(size, dtype=t.uint8, device=pool.device)
+        elif isinstance(stream, int):
             # memory of the caching allocator belongs to the stream that it was taken on
-            if isinstance(stream, int):
-                raise KvoError(KVO_EINVAL, "a raw stream that is not the current one needs a workspace")
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            raise KvoError(KVO_EINVAL, "a raw stream that is not the current one needs a workspace")
         else:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    w = _tensor(workspace, "workspace", torch.uint8, dev, (None,))
-    M, n_w = block_table.shape[1], workspace.shape[0]
-    f = lib().kvo_paged_attend
-    return _on(dev, stream, lambda s: f(p, n_blocks, block_tokens, format, t, M, kv, cu, R, q, T, H, float(scale),
-                                        window, sinks, o, e, w, n_w, st, s))
+            with t.cuda.stream(stream):
+                workspace = t.empty(size, dtype=t.uint8, device=pool.device)
+    else:
+        size = _sizes(workspace, "workspace", 1)[0][0]
+    _launch(lib().kvo_paged_attend, (
+        p, n_blocks, block_tokens, format, _dev(block_table, "block_table", i32, d, (R, M)), M,
+        _dev(kv_lens, "kv_lens", i32, d, (R,)), _dev(cu_tokens, "cu_tokens", i32, d, (R + 1,)), R,
+        _dev(queries, "queries", _types16, d, (T, H, 576)), T, H, float(scale), window, sinks,
+        _dev(out, "out", _types16, d, (T, H, 512)), None if lse is None else _dev(lse, "lse", t.float32, d, (T, H)),
+        _dev(workspace, "workspace", t.uint8, d, (size,)), size,
+        None if status is None else _dev(status, "status", i32, d, (1,))), d, stream)
 
 
 class Kvo:
