@@ -440,6 +440,7 @@ int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, i
   a.pool = static_cast<const uint8_t*>(pool);
   a.n_blocks = n_blocks;
   a.B = block_tokens;
+  a.b_shift = (block_tokens & (block_tokens - 1)) == 0 ? __builtin_ctz((unsigned)block_tokens) : -1;
   a.M = max_blocks;
   a.R = n_requests;
   a.table = block_table;

@@ -95,6 +95,7 @@ struct PagedAttendArgs {
   const uint8_t* pool;
   int64_t n_blocks;
   int32_t B, M, R;
+  int32_t b_shift;         // log2(B), -1 if B is no power of two
   const int32_t* table;    // [R][M]
   const int32_t* kv_lens;  // [R]
   const int32_t* cu;       // [R + 1]

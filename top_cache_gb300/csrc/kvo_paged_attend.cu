@@ -38,12 +38,13 @@
 // Every wait is bounded; when one expires the error word is set and the roles
 // stop.
 //
-// Split.  A schedule kernel lists the tiles with their blocks.  Few tiles (at
-// most kListTiles): the list's blocks are cut evenly over the CTAs, whatever
-// tiles they cross, so one long request fills the GPU; a tile that no CTA has
-// alone leaves partial (O, m, l) in the workspace, at most two per CTA, and a
-// third kernel joins them in CTA order.  Many tiles: CTA c takes tiles c, c +
-// CTAs, ... whole (neighbours cost alike).  Results do not depend on timing.
+// Split.  A schedule kernel lists the tiles with their blocks.  If whole tiles
+// would leave CTAs idle (few tiles, or uneven ones), the list's blocks are cut
+// evenly over the CTAs, whatever tiles they cross, so one long request fills the
+// GPU; a tile that no CTA has alone leaves partial (O, m, l) in the workspace, at
+// most two per CTA, and a third kernel joins them in CTA order.  Else CTA c takes
+// tiles c, c + CTAs, ... (neighbours cost alike).  Results do not depend on
+// timing.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -65,6 +66,9 @@ constexpr int kSlabs = kRow / 64;    // 9: eight of the value, then rope
 constexpr int kListTiles = 2048;     // most tiles that are listed and split
 constexpr int kTileCost = 1;         // a tile's own cost, in blocks (queries in, output out)
 constexpr int kMinShare = 2;         // least units a CTA is given when the list is split
+// What splitting over `used` of the CTAs costs, in blocks' time: one more launch that does something, and the parts
+// written and read (one or two of N x 2 KB a CTA).
+__device__ __forceinline__ int64_t split_cost(int N, int used, int workers) { return 2 + (int64_t)(N / 12) * used / workers; }
 constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr uint32_t kSlab = kBlk * 128;       // bytes of one slab of a block
@@ -87,8 +91,8 @@ struct Shape {
   static constexpr uint32_t kRingOff = kSlabs * kQSlab;
   static constexpr uint32_t kRopeOff = kRingOff + kRing * kPair;
   static constexpr uint32_t kPOff = kSharedP ? kRopeOff : kRopeOff + kSlab;
-  static constexpr uint32_t kPBytes = kSharedP ? 0u : N * 256u;
-  static constexpr uint32_t kMiscOff = kRopeOff + kSlab + kPBytes;
+  static constexpr uint32_t kPBytes = kSharedP ? kSlab : N * 256u;
+  static constexpr uint32_t kMiscOff = kPOff + kPBytes;
   // misc: less running maxima, query factors, row positions [2][N], a block's maxima and the tile's sums [8][NC],
   // factors of a move of the running maximum [N], 1 / l [N]
   static constexpr uint32_t kMiscBytes = (3 * 2 * N + 2 * 8 * kNC + 2 * N) * 4;
@@ -103,22 +107,25 @@ struct Shape {
 };
 
 // ---- tcgen05 ------------------------------------------------------------------------------
-// Shared-memory matrix descriptor, 128-byte swizzle (byte offsets in 16-byte units).
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory matrix descriptor, 128-byte swizzle: start address and leading offset (in 16-byte units) in the low
+// word; the high word is the same for every operand here: rows (or tokens) in groups of 8, 1 KB apart.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t sdesc(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3FFFu) | (((lead >> 4) & 0x3FFFu) << 16);
 }
 // Instruction descriptor of kind::f16: A and B both bf16 or both f16, fp32 D.
 constexpr uint32_t idesc(bool bf16, int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) |
          ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// Issued by the lane whose `el` is set; the warp runs it uniformly.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t el) {
+// Issued by the lane whose `el` is set; the warp runs it uniformly.  The operands live in uniform registers, and moving
+// one there costs more than the MMA's issue: only the descriptors' low words vary.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t el) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(el)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(el), "n"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t el) {
@@ -161,6 +168,20 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[NC]) {
   for (int c = 0; c < NC; c += 8) tmem_ld8(t + (uint32_t)c, v + c);
 }
 
+// Bounded wait on a phase parity; false when limit_ns has passed, or another role has given up.  Reading the timer costs more than most waits here
+// last, so it starts late.
+__device__ __forceinline__ bool phase_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                           const volatile uint32_t* abort = nullptr) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns || (abort && *abort != 0u)) return false;
+    }
+  }
+}
 // ---- shared memory -------------------------------------------------------------------------
 // 16-byte chunk c (0..7) of row r in a 128-byte-swizzled slab (1 KB aligned).
 __device__ __forceinline__ uint32_t swz(uint32_t slab, int r, int c) {
@@ -329,11 +350,11 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAtte
   __shared__ int64_t warp_sums[33];
   __shared__ int32_t off[kMaxRequests + 1];      // tiles before each request
   __shared__ int32_t before[kListTiles];         // units before each tile
-  __shared__ int32_t n_shared;
+  __shared__ int32_t n_shared, most;
   launch_dependents();
   const int tid = threadIdx.x;
   int64_t total = 0, sum;
-  if (tid == 0) n_shared = 0;
+  if (tid == 0) n_shared = most = 0;
   for (int base = 0; base < a.R; base += kSchedThreads) {
     const int r = base + tid;
     const int64_t n = r < a.R ? (request_rows(a, r) + N - 1) / N : 0;
@@ -342,15 +363,14 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAtte
     total += sum;
   }
   const int n_tiles = (int)total;
-  const bool listed = n_tiles <= kListTiles;
   if (tid == 0) {
     a.tile_off[a.R] = n_tiles;
-    a.head[kHdListed] = listed ? 1 : 0;
+    a.head[kHdListed] = 0;
     a.head[kHdTiles] = n_tiles;
     *a.status = 0u;
   }
   __syncthreads();
-  if (!listed) return;
+  if (n_tiles > kListTiles) return;
   // thread i lists tiles 2 i and 2 i + 1
   int cost[2] = {0, 0};
 #pragma unroll
@@ -361,6 +381,7 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAtte
       Seg s;
       tile_of(a, N, r, (i - off[r]) * N, s);
       cost[k] = s.nblk + kTileCost;
+      atomicMax(&most, cost[k]);
       a.tiles[i] = make_int4(r, s.row0, s.nblk, 0);
     }
   }
@@ -372,6 +393,10 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAtte
   const int64_t share = max((int64_t)kMinShare, (units + a.workers - 1) / a.workers);
   const int used = (int)min((int64_t)a.workers, (units + share - 1) / share);
   __syncthreads();
+  // whole tiles, if the longest of them for every round take no longer than even shares and what joining them costs
+  if ((int64_t)((n_tiles + a.workers - 1) / a.workers) * most <=
+      (units + used - 1) / max(used, 1) + split_cost(N, used, a.workers))
+    return;
   // CTA w starts at unit w * units / used
   for (int w = tid; w < used; w += kSchedThreads) {
     const int64_t u = (int64_t)w * units / used;
@@ -391,6 +416,7 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAtte
   __syncthreads();
   if (tid == 0) {
     a.start[used] = make_int2(n_tiles, 0);
+    a.head[kHdListed] = 1;
     a.head[kHdWorkers] = used;
     a.head[kHdShared] = n_shared;
   }
@@ -433,9 +459,11 @@ __device__ __forceinline__ void scales2(uint32_t b, uint32_t& s0, uint32_t& s1) 
   s1 = __byte_perm(h, h, 0x3232);
 }
 
+// Entry of a request's block table that token t is in.
+__device__ __forceinline__ int entry_of(const PagedAttendArgs& a, int t) { return a.b_shift >= 0 ? t >> a.b_shift : t / a.B; }
 // Token t's row of the pool (-1: its block is not mapped).
 __device__ __forceinline__ int64_t pool_row(const PagedAttendArgs& a, const int32_t* table, int t) {
-  const int j = t / a.B;
+  const int j = entry_of(a, t);
   const int32_t b = __ldg(table + j);
   return b < 0 || (int64_t)b >= a.n_blocks ? -1 : (int64_t)b * a.B + (t - j * a.B);
 }
@@ -510,9 +538,9 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(&B.tmem), 0);
-  // a warp's lanes wait together; false: the wait expired (or another role gave up)
+  // a warp's lanes wait together; false: give up
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(kFull, mbar_wait(bar, parity & 1u, a.wait_ns)) && !__any_sync(kFull, *abort_flag != 0u);
+    return __all_sync(kFull, phase_wait(bar, parity & 1u, a.wait_ns, abort_flag));
   };
 
   grid_wait();
@@ -578,26 +606,45 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       }
       if (!ok) fail();
       // the CTA may not end before its copies have landed (they have, unless a role gave up)
-      bool landed = tc == 0 || mbar_wait(&B.q_full, (uint32_t)(tc - 1) & 1u, a.wait_ns);
-      if (ropes > 0) landed = mbar_wait(&B.r_full, (uint32_t)(ropes - 1) & 1u, a.wait_ns) && landed;
+      bool landed = tc == 0 || phase_wait(&B.q_full, (uint32_t)(tc - 1) & 1u, a.wait_ns);
+      if (ropes > 0) landed = phase_wait(&B.r_full, (uint32_t)(ropes - 1) & 1u, a.wait_ns) && landed;
       for (int x = max(0, pairs - C::kRing); x < pairs; ++x)
-        landed = mbar_wait(&B.e_full[x % C::kRing], (uint32_t)(x / C::kRing) & 1u, a.wait_ns) && landed;
+        landed = phase_wait(&B.e_full[x % C::kRing], (uint32_t)(x / C::kRing) & 1u, a.wait_ns) && landed;
       if (!landed) fail();
     } else {
       // ---- producers, 4 bits ------------------------------------------------------------
+      // thread (token, side): slab 2 i + side of pair i
       const int pt = tid - kSoftThreads, tok = pt >> 1, side = pt & 1;
+      // 16-byte chunk c of this token's 128 bytes of a slab lies at (chunk0 + slab) ^ (c << 4)
+      const uint32_t chunk0 = (uint32_t)tok * 128u + ((uint32_t)(tok & 7) << 4);
       Codes k{};
+      // The block whose cache block is being looked up runs two blocks ahead of the one being expanded, that whose
+      // codes are being read one.
+      Walk<N> far = walk;
+      Seg fs;
+      int fb = 0, f_in = 0;
+      int32_t f_entry = -1;
+      bool f_more = far.next(a, fs);
+      while (f_more && fs.b0 >= fs.b1) f_more = far.next(a, fs);
+      fb = fs.b0 - 1;
+      auto look_up = [&]() {  // the next block's entry of the table
+        if (!f_more) return;
+        if (++fb >= fs.b1) {
+          do f_more = far.next(a, fs); while (f_more && fs.b0 >= fs.b1);
+          if (!f_more) return;
+          fb = fs.b0;
+        }
+        const int t = fs.block(fb) * kBlk + tok, j = entry_of(a, t);
+        f_in = t - j * a.B;
+        f_entry = fs.any_sees(t) ? __ldg(a.table + (int64_t)fs.r * a.M + j) : -1;
+      };
       const uint8_t *crow = nullptr, *srow = nullptr;  // null: zeros
-      auto locate = [&](const Seg& sg, int b) {
-        const int t = sg.block(b) * kBlk + tok;
-        const int64_t row = sg.any_sees(t) ? pool_row(a, a.table + (int64_t)sg.r * a.M, t) : -1;
+      auto locate = [&]() {
         crow = nullptr;
-        if (row >= 0) {
-          const int64_t blk = row / a.B;
-          const int in = (int)(row - blk * a.B);
-          const uint8_t* base = a.pool + blk * ((int64_t)a.B * kRowBytesQ4);
-          crow = base + (int64_t)in * kCodeBytes;
-          srow = base + (int64_t)a.B * kCodeBytes + in * kGroups;
+        if (f_entry >= 0 && (int64_t)f_entry < a.n_blocks) {
+          const uint8_t* base = a.pool + (int64_t)f_entry * (a.B * kRowBytesQ4);
+          crow = base + f_in * kCodeBytes;
+          srow = base + a.B * kCodeBytes + f_in * kGroups;
         }
       };
       auto load_pair = [&](int i) {
@@ -618,16 +665,19 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           k.rs = __ldg(reinterpret_cast<const uint16_t*>(srow + 32 + side * 2));
         }
       };
-      bool ok = true, have = walk.next(a, s);
-      while (have && s.b0 >= s.b1) have = walk.next(a, s);
-      if (have) {
-        locate(s, s.b0);
+      look_up();
+      bool pre = f_more;
+      if (pre) {
+        locate();
 #pragma unroll
         for (int i = 0; i < 4; ++i) load_pair(i);
         load_rope();
+        look_up();
       }
-      while (ok && have) {
-        if (tc >= 1 && !wait(&B.q_free, (uint32_t)(tc - 1))) { fail(); break; }
+      bool ok = true;
+      while (ok && walk.next(a, s)) {
+        if (s.b0 >= s.b1) continue;
+        if (tc >= 1 && !wait(&B.q_free, (uint32_t)(tc - 1))) { ok = false; break; }
         // queries: one warp per row; scaled by 2^-e so that the largest magnitude is in [2^14, 2^15)
         for (int r = warp - kProd0; r < N; r += C::kProdWarps) {
           const uint4* src = reinterpret_cast<const uint4*>(a.q + (s.grow + r) * kRow);
@@ -661,77 +711,67 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           }
           if (lane == 0) q_mul[(tc & 1) * N + r] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
         }
-        fence_proxy_async_smem();
         mbar_arrive(&B.q_full);
         ++tc;
-        Seg nx = s;
-        bool more = true;
         for (int b = s.b0; b < s.b1; ++b, ++g) {
-          // the block after this one, of this segment or of the next
-          bool pre = true;
-          if (b + 1 < s.b1) {
-            locate(s, b + 1);
-          } else {
-            do more = walk.next(a, nx); while (more && nx.b0 >= nx.b1);
-            pre = more;
-            if (more) locate(nx, nx.b0);
+          pre = f_more;
+          if (pre) {
+            locate();
+            look_up();
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int x = 4 * g + i, slot = x % C::kRing, use = x / C::kRing;
             if (use >= 1 && !wait(&B.e_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
-            const uint32_t dst = sb + C::kRingOff + (uint32_t)slot * kPair + (uint32_t)side * kSlab;
+            const uint32_t dst = sb + C::kRingOff + (uint32_t)slot * kPair + (uint32_t)side * kSlab + chunk0;
             uint32_t sc[4];
             scales2(k.s[i] & 0xffffu, sc[0], sc[1]);
             scales2(k.s[i] >> 16, sc[2], sc[3]);
-            // a token's two threads start four chunks apart: the slabs are 16 KB apart, the same banks
-            const uint32_t cw[8] = {k.c[i][0].x, k.c[i][0].y, k.c[i][0].z, k.c[i][0].w,
-                                    k.c[i][1].x, k.c[i][1].y, k.c[i][1].z, k.c[i][1].w};
+            // a token's two threads start four chunks apart: the slabs share their banks
+            const uint32_t turn = (uint32_t)side << 6;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int o = side ? (q ^ 2) : q;
-              const uint32_t w0 = side ? cw[2 * (q ^ 2)] : cw[2 * q], w1 = side ? cw[2 * (q ^ 2) + 1] : cw[2 * q + 1];
+              const uint4 c0 = k.c[i][q >> 1], c1 = k.c[i][(q >> 1) ^ 1];
+              const bool other = side;
+              const uint4 c = other ? c1 : c0;
               uint4 lo, hi;
-              expand16(w0, w1, side ? sc[q ^ 2] : sc[q], lo, hi);
-              st_v4(swz(dst, tok, 2 * o), lo);
-              st_v4(swz(dst, tok, 2 * o + 1), hi);
+              expand16(q & 1 ? c.z : c.x, q & 1 ? c.w : c.y, other ? sc[q ^ 2] : sc[q], lo, hi);
+              st_v4((dst ^ turn) ^ (uint32_t)(2 * q) << 4, lo);
+              st_v4((dst ^ turn) ^ (uint32_t)(2 * q + 1) << 4, hi);
             }
-            fence_proxy_async_smem();
             mbar_arrive(&B.e_full[slot]);
             if (pre) load_pair(i);
           }
           if (!ok) break;
           if (g >= 1 && !wait(&B.r_free, (uint32_t)(g - 1))) { ok = false; break; }
-          {
-            uint32_t s0, s1;
-            scales2(k.rs, s0, s1);
-            uint4 lo, hi;
-            expand16(k.rc.x, k.rc.y, s0, lo, hi);
-            st_v4(swz(sb + C::kRopeOff, tok, 4 * side), lo);
-            st_v4(swz(sb + C::kRopeOff, tok, 4 * side + 1), hi);
-            expand16(k.rc.z, k.rc.w, s1, lo, hi);
-            st_v4(swz(sb + C::kRopeOff, tok, 4 * side + 2), lo);
-            st_v4(swz(sb + C::kRopeOff, tok, 4 * side + 3), hi);
-            fence_proxy_async_smem();
-            mbar_arrive(&B.r_full);
-            if (pre) load_rope();
-          }
+          const uint32_t dst = (sb + C::kRopeOff + chunk0) ^ (uint32_t)side << 6;
+          uint32_t s0, s1;
+          scales2(k.rs, s0, s1);
+          uint4 lo, hi;
+          expand16(k.rc.x, k.rc.y, s0, lo, hi);
+          st_v4(dst, lo);
+          st_v4(dst ^ 1u << 4, hi);
+          expand16(k.rc.z, k.rc.w, s1, lo, hi);
+          st_v4(dst ^ 2u << 4, lo);
+          st_v4(dst ^ 3u << 4, hi);
+          mbar_arrive(&B.r_full);
+          if (pre) load_rope();
         }
-        if (!ok) fail();
-        s = nx;
-        have = more;
       }
+      if (!ok) fail();
     }
   } else if (warp == kMmaWarp) {
     // ---- MMA issue ------------------------------------------------------------------------
+    // The proxy fences stand here, behind the waits, for the bytes that other threads wrote with ordinary stores: in
+    // the writers, a fence waits for whatever the thread still has to load.
     const uint32_t el = elect();
     constexpr uint32_t kIdS = idesc(!kQ4, kBlk, N, false, false);
     constexpr uint32_t kIdO = idesc(!kQ4, kBlk, N, true, C::kSharedP);
-    const uint64_t ring_k = sdesc(sb + C::kRingOff, 16, 1024);      // K-major slabs
-    const uint64_t ring_v = sdesc(sb + C::kRingOff, kSlab, 1024);   // MN-major: two slabs, 128 value elements
-    const uint64_t rope = sdesc(sb + C::kRopeOff, 16, 1024);
-    const uint64_t qd = sdesc(sb + C::kQOff, 16, 1024);
-    const uint64_t pd = sdesc(sb + C::kPOff, 16, 1024);
+    const uint32_t ring_k = sdesc(sb + C::kRingOff, 16);     // K-major slabs
+    const uint32_t ring_v = sdesc(sb + C::kRingOff, kSlab);  // MN-major: two slabs, 128 value elements
+    const uint32_t rope = sdesc(sb + C::kRopeOff, 16);
+    const uint32_t qd = sdesc(sb + C::kQOff, 16);
+    const uint32_t pd = sdesc(sb + C::kPOff, 16);
     bool ok = true;
     while (ok && walk.next(a, s)) {
       if (s.b0 >= s.b1) continue;
@@ -746,8 +786,8 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           tc_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ss(dS, ring_k + (uint64_t)(((uint32_t)slot * kPair + (uint32_t)(kk >> 2) * kSlab) >> 4) + (uint64_t)((kk & 3) * 2),
-                   qd + (uint64_t)(((uint32_t)(2 * i + (kk >> 2)) * C::kQSlab) >> 4) + (uint64_t)((kk & 3) * 2), kIdS,
+            mma_ss(dS, ring_k + (((uint32_t)slot * kPair + (uint32_t)(kk >> 2) * kSlab) >> 4) + (uint32_t)((kk & 3) * 2),
+                   qd + (((uint32_t)(2 * i + (kk >> 2)) * C::kQSlab) >> 4) + (uint32_t)((kk & 3) * 2), kIdS,
                    (i | kk) ? 1u : 0u, el);
         }
         if (!ok || !wait(&B.r_full, (uint32_t)g)) { ok = false; break; }
@@ -755,7 +795,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         tc_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ss(dS, rope + (uint64_t)(kk * 2), qd + (uint64_t)((8u * C::kQSlab) >> 4) + (uint64_t)(kk * 2), kIdS, 1u, el);
+          mma_ss(dS, rope + (uint32_t)(kk * 2), qd + ((8u * C::kQSlab) >> 4) + (uint32_t)(kk * 2), kIdS, 1u, el);
         mma_commit(&B.s_full, el);
         if (!C::kSharedP) mma_commit(&B.r_free, el);
         if (b + 1 == s.b1) mma_commit(&B.q_free, el);
@@ -769,9 +809,9 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             // P^T: N = 64 MN-major (16 tokens are 2 KB), else K-major (64 tokens a slab of N rows)
-            const uint64_t p = C::kSharedP ? pd + (uint64_t)((uint32_t)kk * 2048u >> 4)
-                                           : pd + (uint64_t)(((uint32_t)(kk >> 2) * (N * 128u)) >> 4) + (uint64_t)((kk & 3) * 2);
-            mma_ss(tmem + (uint32_t)(i * N), ring_v + (uint64_t)(((uint32_t)slot * kPair + (uint32_t)kk * 2048u) >> 4), p, kIdO,
+            const uint32_t p = C::kSharedP ? pd + ((uint32_t)kk * 2048u >> 4)
+                                           : pd + (((uint32_t)(kk >> 2) * (N * 128u)) >> 4) + (uint32_t)((kk & 3) * 2);
+            mma_ss(tmem + (uint32_t)(i * N), ring_v + (((uint32_t)slot * kPair + (uint32_t)kk * 2048u) >> 4), p, kIdO,
                    (b > s.b0 || kk > 0) ? 1u : 0u, el);
           }
           mma_commit(&B.e_free[slot], el);
@@ -784,14 +824,13 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
     if (!ok) fail();
     // everything issued is complete before TMEM is freed (the tensor pipe waits on nothing outside this CTA)
     mma_commit(&B.fin, el);
-    if (!__all_sync(kFull, mbar_wait(&B.fin, 0, a.wait_ns > 2000000000ull ? a.wait_ns : 2000000000ull))) fail();
+    if (!__all_sync(kFull, phase_wait(&B.fin, 0, a.wait_ns > 2000000000ull ? a.wait_ns : 2000000000ull))) fail();
   } else {
     // ---- softmax ---------------------------------------------------------------------------
     const int st = tid, hw = warp >> 2, quad = warp & 3;  // half of the rows; lane quadrant
     const int tok = 32 * quad + lane;                     // this thread's token of a block
     const int c0 = hw * NC;                               // its first row of the tile
     const uint32_t lane_addr = (uint32_t)(32 * quad) << 16;
-    const uint32_t sS = tmem + lane_addr + C::kColS + (uint32_t)c0;
     const uint32_t bar_half = 1u + (uint32_t)hw;          // 128 threads with the same rows
     // A warp whose wait expires still meets the others of its half at their next barrier and tells them there, so
     // that all four leave together: the flag of a barrier is set before it and read after it, and no warp can be two
@@ -857,6 +896,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         }
         dead = dead || !wait(&B.s_full, (uint32_t)g);
         tc_after();
+        const uint32_t sS = tmem + lane_addr + C::kColS + (uint32_t)c0;
         float v[NC];
         // v: scores in log2 units less the running maximum (plus kBias); -inf where hidden.  Where the maximum has
         // just moved the product is rounded as the maximum was, so that its own score is no less than 0 however
@@ -962,7 +1002,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           // comes of either), so the score of any one query tells, and a position that sees the row is not misled.
           uint32_t edge = __ballot_sync(kFull, !all && odd);
           const int i = 2 * hw + (lane >> 4), x4 = 4 * g + i;  // this half's two pairs: 32 chunks of 8 elements
-          if (!mbar_wait(&B.e_full[x4 % C::kRing], (uint32_t)(x4 / C::kRing) & 1u, a.wait_ns)) fail();  // (S^T has read it)
+          if (!phase_wait(&B.e_full[x4 % C::kRing], (uint32_t)(x4 / C::kRing) & 1u, a.wait_ns)) fail();  // (S^T has read it)
           const uint32_t slab = sb + C::kRingOff + (uint32_t)(x4 % C::kRing) * kPair + (uint32_t)((lane >> 3) & 1) * kSlab;
           while (edge) {
             const int r = 32 * quad + __ffs(edge) - 1;
@@ -980,7 +1020,6 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
             if (bad) st_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
           }
         }
-        fence_proxy_async_smem();
         tc_before();
         mbar_arrive(&B.p_full);
       }
@@ -1051,46 +1090,75 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// join: the parts of a tile that several CTAs share, in CTA order.  128 threads
-// a row, four value elements each, several parts in flight.
+// join: the parts of a tile that several CTAs share, in a fixed order.  128
+// threads have a row, four value elements each.  Many rows: four rows per CTA;
+// few (one long request): the four groups of a CTA take every fourth part of one
+// row and meet in shared memory.
 // ---------------------------------------------------------------------------
-constexpr int kJoinRows = 4;  // rows per CTA
-constexpr int kJoinThreads = kJoinRows * kVal / 4;
+constexpr int kJoinGroups = 4;
+constexpr int kJoinThreads = kJoinGroups * kVal / 4;
 
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArgs a, float bias) {
+  __shared__ float4 acc[kJoinGroups][kVal / 4];
+  __shared__ float sum[kJoinGroups];
   grid_wait();
   if (a.head[kHdListed] == 0) return;
-  const int item = (int)blockIdx.x * kJoinRows + (int)threadIdx.x / (kVal / 4), col = threadIdx.x % (kVal / 4);
-  const int row = item % N;
-  if (item / N >= a.head[kHdShared]) return;
-  const int4 sh = a.shared[item / N];  // tile, first CTA, last CTA, slot of the first one's part (0 for the others)
-  const int4 d = a.tiles[sh.x];
-  Seg s;
-  tile_of(a, N, d.x, d.y, s);
-  if (row >= s.nrows) return;
-  auto part = [&](int w) -> int64_t { return (int64_t)w * 2 + (w == sh.y ? sh.w : 0); };
-  float m = kNone;
+  const int group = (int)threadIdx.x / (kVal / 4), col = threadIdx.x % (kVal / 4);
+  const int items = a.head[kHdShared] * N;
+  const int groups = items >= kJoinGroups * (int)gridDim.x ? 1 : kJoinGroups;  // that work on one row
+  const int per_cta = kJoinGroups / groups;
+  for (int first = (int)blockIdx.x * per_cta; first < items; first += (int)gridDim.x * per_cta) {
+    const int item = min(first + (per_cta > 1 ? group : 0), items - 1), row = item % N;
+    const int4 sh = a.shared[item / N];  // tile, first CTA, last CTA, slot of the first one's part (0 for the others)
+    const int4 d = a.tiles[sh.x];
+    Seg s;
+    tile_of(a, N, d.x, d.y, s);
+    const bool in = row < s.nrows && first + (per_cta > 1 ? group : 0) < items;
+    auto part = [&](int w) -> int64_t { return (int64_t)w * 2 + (w == sh.y ? sh.w : 0); };
+    float m = kNone;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (in) {
 #pragma unroll 8
-  for (int w = sh.y; w <= sh.z; ++w) m = fmaxf(m, a.part_ml[part(w) * 2 * N + row]);
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+      for (int w = sh.y; w <= sh.z; ++w) m = fmaxf(m, a.part_ml[part(w) * 2 * N + row]);
 #pragma unroll 8
-  for (int w = sh.y; w <= sh.z; ++w) {
-    const int64_t p = part(w);
-    const float4 y = reinterpret_cast<const float4*>(a.part_o + (p * N + row) * kVal)[col];
-    const float f = ex2(a.part_ml[p * 2 * N + row] - m);
-    l += f * a.part_ml[p * 2 * N + N + row];
-    x.x += f * y.x;
-    x.y += f * y.y;
-    x.z += f * y.z;
-    x.w += f * y.w;
+      for (int w = sh.y + (groups > 1 ? group : 0); w <= sh.z; w += groups) {
+        const int64_t p = part(w);
+        const float4 y = reinterpret_cast<const float4*>(a.part_o + (p * N + row) * kVal)[col];
+        const float f = ex2(a.part_ml[p * 2 * N + row] - m);
+        l += f * a.part_ml[p * 2 * N + N + row];
+        x.x += f * y.x;
+        x.y += f * y.y;
+        x.z += f * y.z;
+        x.w += f * y.w;
+      }
+    }
+    if (groups > 1) {
+      __syncthreads();  // the last row's sums have been read
+      acc[group][col] = x;
+      if (col == 0) sum[group] = l;
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int k = 1; k < kJoinGroups; ++k) {
+          const float4 y = acc[k][col];
+          x.x += y.x;
+          x.y += y.y;
+          x.z += y.z;
+          x.w += y.w;
+          l += sum[k];
+        }
+      }
+    }
+    if (in && (groups == 1 || group == 0)) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const __nv_bfloat162 h0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), h1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+      reinterpret_cast<uint2*>(a.out + (s.grow + row) * kVal)[col] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+      if (col == 0 && a.lse) a.lse[s.grow + row] = l == 0.f ? -INFINITY : (m - bias + log2f(l)) * 0.6931471805599453f;
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const __nv_bfloat162 h0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), h1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-  reinterpret_cast<uint2*>(a.out + (s.grow + row) * kVal)[col] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-  if (col == 0 && a.lse) a.lse[s.grow + row] = l == 0.f ? -INFINITY : (m - bias + log2f(l)) * 0.6931471805599453f;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1154,7 +1222,7 @@ cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
   schedule_paged_kernel<<<1, kSchedThreads, 0, s>>>(a, N);
   e = cudaGetLastError();
   if (e == cudaSuccess) e = launch_after(attend_paged_kernel<N, kQ4>, a.workers, C::kThreads, C::kSmem, s, a, maps);
-  if (e == cudaSuccess) e = launch_after(join_paged_kernel<N>, a.workers * N / kJoinRows, kJoinThreads, 0, s, a, C::kBias);
+  if (e == cudaSuccess) e = launch_after(join_paged_kernel<N>, 4 * a.workers, kJoinThreads, 0, s, a, C::kBias);
   return e;
 }
 
