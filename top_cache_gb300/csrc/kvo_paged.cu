@@ -168,31 +168,28 @@ __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs 
 constexpr int kRowsPerCta = 8;
 constexpr int kRowThreads = kRowsPerCta * kGroups;
 
-__device__ __forceinline__ uint8_t* q4_codes(uint8_t* pool, int64_t slot, int B) {
-  return pool + (slot / B) * ((int64_t)B * kRowBytesQ4) + (slot % B) * kCodeBytes;
-}
-__device__ __forceinline__ uint8_t* q4_scales(uint8_t* pool, int64_t slot, int B) {
-  return pool + (slot / B) * ((int64_t)B * kRowBytesQ4) + (int64_t)B * kCodeBytes + (slot % B) * kGroups;
-}
-
-// E2M1 code of a >= 0 (already divided by the scale): round to nearest, a tie
-// to the even code, above 5 to the largest value.
-__device__ __forceinline__ uint32_t e2m1_of(float a) {
-  return (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) + (uint32_t)(a >= 1.75f) +
-         (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.f);
+// Two codes (low four bits: x) of values already multiplied by 1 / scale in fp32.  A bf16 value that is not exactly on
+// the border between two codes is off it by at least 2^-8 of it, one that is may be off by the reciprocal's and the
+// product's rounding, 2^-22 of it: rounding to 11 bits first puts it back on the border, and moves no other across.
+// The conversion rounds to nearest, a tie to the even code, and saturates.
+__device__ __forceinline__ uint32_t e2m1_pair(float x, float y) {
+  const float2 r = __half22float2(__floats2half2_rn(x, y));
+  uint32_t c;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tmov.b32 %0, {t, 0, 0, 0};\n\t}" : "=r"(c) : "f"(r.x), "f"(r.y));
+  return c;
 }
 
 template <bool kQ4>
 __global__ void __launch_bounds__(kRowThreads) write_paged_kernel(PagedRowsArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x / kGroups;
-  const int g = threadIdx.x % kGroups;
+  const uint32_t local = threadIdx.x / kGroups, g = threadIdx.x % kGroups;
+  const int64_t i = (int64_t)blockIdx.x * kRowsPerCta + local;
   if (i >= a.n) return;
-  const int64_t slot = __ldg(a.slots + i);
-  if (slot < 0 || slot >= a.pool_rows) return;
+  const int32_t slot = __ldg(a.slots + i);
   const uint4* src = reinterpret_cast<const uint4*>(a.rows + i * kRow + g * kGroup);
-  const uint4 x0 = __ldg(src), x1 = __ldg(src + 1);
+  const uint4 x0 = __ldcs(src), x1 = __ldcs(src + 1);
+  if (slot < 0 || slot >= a.pool_rows) return;
   if (!kQ4) {
-    uint4* dst = reinterpret_cast<uint4*>(a.pool + slot * kRowBytes16 + g * kGroup * 2);
+    uint4* dst = reinterpret_cast<uint4*>(a.pool + (int64_t)slot * kRowBytes16 + g * kGroup * 2);
     dst[0] = x0;
     dst[1] = x1;
     return;
@@ -201,62 +198,58 @@ __global__ void __launch_bounds__(kRowThreads) write_paged_kernel(PagedRowsArgs 
   // the largest magnitude, by its bits: NaN above infinity above every finite value
   uint32_t top = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-  uint2 codes = make_uint2(0u, 0u);
-  uint8_t sbits = 0x7f;  // a group that is not finite reads as NaN
+  for (int k = 0; k < 8; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
+  top = max(top & 0xffffu, top >> 16);
+  uint32_t c[2] = {0u, 0u};
+  uint32_t sbits = 0x7f;  // a group that is not finite reads as NaN
   if (top < 0x7f80u) {
     const float amax = __uint_as_float(top << 16);
-    sbits = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.f), __NV_SATFINITE, __NV_E4M3);
-    const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(sbits, __NV_E4M3)));
+    sbits = __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.f), __NV_SATFINITE, __NV_E4M3);
+    const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((uint8_t)sbits, __NV_E4M3)));
     if (s > 0.f) {
-      uint32_t c[2] = {0u, 0u};
+      const float inv = __frcp_rn(s);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t lo = e2m1_of(__fdiv_rn(fabsf(bf_lo(w[k])), s)) | ((w[k] >> 12) & 8u);
-        const uint32_t hi = e2m1_of(__fdiv_rn(fabsf(bf_hi(w[k])), s)) | ((w[k] >> 28) & 8u);
-        c[k >> 2] |= (lo | (hi << 4)) << (8 * (k & 3));
-      }
-      codes = make_uint2(c[0], c[1]);
+      for (int k = 0; k < 8; ++k) c[k >> 2] |= e2m1_pair(bf_lo(w[k]) * inv, bf_hi(w[k]) * inv) << (8 * (k & 3));
     }
   }
-  *reinterpret_cast<uint2*>(q4_codes(a.pool, slot, a.B) + g * (kGroup / 2)) = codes;
-  q4_scales(a.pool, slot, a.B)[g] = sbits;
+  const uint32_t blk = (uint32_t)slot / (uint32_t)a.B, in = (uint32_t)slot - blk * (uint32_t)a.B;
+  uint8_t* base = a.pool + (int64_t)blk * ((int64_t)a.B * kRowBytesQ4);
+  *reinterpret_cast<uint2*>(base + in * kCodeBytes + g * (kGroup / 2)) = make_uint2(c[0], c[1]);
+  base[a.B * kCodeBytes + in * kGroups + g] = (uint8_t)sbits;
 }
 
 template <bool kQ4>
 __global__ void __launch_bounds__(kRowThreads) read_paged_kernel(PagedRowsArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x / kGroups;
-  const int g = threadIdx.x % kGroups;
+  const uint32_t local = threadIdx.x / kGroups, g = threadIdx.x % kGroups;
+  const int64_t i = (int64_t)blockIdx.x * kRowsPerCta + local;
   if (i >= a.n) return;
-  const int64_t slot = __ldg(a.slots + i);
+  const int32_t slot = __ldg(a.slots + i);
   if (slot < 0 || slot >= a.pool_rows) return;
   uint4* dst = reinterpret_cast<uint4*>(a.rows + i * kRow + g * kGroup);
   if (!kQ4) {
-    const uint4* src = reinterpret_cast<const uint4*>(a.pool + slot * kRowBytes16 + g * kGroup * 2);
+    const uint4* src = reinterpret_cast<const uint4*>(a.pool + (int64_t)slot * kRowBytes16 + g * kGroup * 2);
     const uint4 x0 = src[0], x1 = src[1];
     dst[0] = x0;
     dst[1] = x1;
     return;
   }
-  const uint2 codes = *reinterpret_cast<const uint2*>(q4_codes(a.pool, slot, a.B) + g * (kGroup / 2));
-  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(q4_scales(a.pool, slot, a.B)[g], __NV_E4M3)));
+  const uint32_t blk = (uint32_t)slot / (uint32_t)a.B, in = (uint32_t)slot - blk * (uint32_t)a.B;
+  const uint8_t* base = a.pool + (int64_t)blk * ((int64_t)a.B * kRowBytesQ4);
+  const uint2 codes = *reinterpret_cast<const uint2*>(base + in * kCodeBytes + g * (kGroup / 2));
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(base[a.B * kCodeBytes + in * kGroups + g], __NV_E4M3)));
   uint32_t w[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint32_t b = ((k < 4 ? codes.x : codes.y) >> (8 * (k & 3))) & 0xffu;
-    // a code's magnitude: exponent field 0 is a multiple of 1/2, else 2^(e - 1) (1 + m / 2)
-    float v[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t c = (b >> (4 * h)) & 15u, e = (c >> 1) & 3u, m = c & 1u;
-      const float x = e == 0u ? 0.5f * (float)m : (float)(2u + m) * 0.25f * (float)(1u << e);
-      v[h] = (c & 8u) ? -x : x;
-    }
-    const __nv_bfloat162 p = __floats2bfloat162_rn(v[0] * s, v[1] * s);  // exact
+    uint32_t h;
+    asm("{\n\t.reg .b8 t, u0, u1, u2;\n\tmov.b32 {t, u0, u1, u2}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+        : "=r"(h)
+        : "r"((k < 4 ? codes.x : codes.y) >> (8 * (k & 3))));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * s, v.y * s);  // exact
     w[k] = *reinterpret_cast<const uint32_t*>(&p);
   }
-  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
 }
 
 template <typename K>
@@ -406,7 +399,7 @@ size_t kvo_paged_attend_workspace_size(int32_t n_requests, int32_t n_tokens, int
   if (n_requests < 1 || n_requests > kvo::paged::kMaxRequests || n_tokens < 0 || n_heads < 1 || n_heads > 8192) return 0;
   int n_sm = 0;
   if (cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
-  return kvo::paged_attend_workspace(n_requests, n_tokens, n_heads, n_sm);
+  return kvo::paged_attend_workspace(n_requests, n_tokens, n_heads, n_sm < kvo::paged::kMaxWorkers ? n_sm : kvo::paged::kMaxWorkers);
 }
 
 int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,
@@ -434,6 +427,7 @@ int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, i
   int dev = 0, n_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return fail(KVO_ECUDA, "no current device");
+  if (n_sm > paged::kMaxWorkers) n_sm = paged::kMaxWorkers;
   if (workspace_bytes < paged_attend_workspace(n_requests, n_tokens, n_heads, n_sm))
     return fail(KVO_EINVAL, "workspace too small");
   PagedAttendArgs a{};
@@ -457,6 +451,7 @@ int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, i
   a.status = status;
   a.wait_ns = 2000000000ull;
   a.workers = n_sm;
+  a.device = dev;
   paged_attend_carve(a, static_cast<uint8_t*>(workspace));
   const cudaError_t e = launch_paged_attend(a, format == KVO_CACHE_Q4, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_cuda_error(e, "paged attention launch");

@@ -26,6 +26,7 @@ constexpr int kCodeBytes = kRow / 2;  // codes of one row
 constexpr int kRowBytesQ4 = kCodeBytes + kGroups;
 constexpr int kRowBytes16 = kRow * 2;
 constexpr int kMaxRequests = 4096;    // per call: the requests' arrays fit shared memory
+constexpr int kMaxWorkers = 256;      // CTAs of the attention launch (one per SM)
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // tokens a block table reaches; rows of a pool are below 2^31
 
 // Exclusive prefix sum over the CTA's threads (kThreads a multiple of 32, at
@@ -108,6 +109,7 @@ struct PagedAttendArgs {
   uint32_t* status;        // error word
   uint64_t wait_ns;
   int32_t workers;         // CTAs of the attention launch
+  int32_t device;
   // workspace
   int32_t* head;           // listed, tiles, CTAs in use, shared tiles
   int32_t* tile_off;       // [R + 1] tiles before each request

@@ -51,6 +51,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "kvo_paged.cuh"
@@ -565,23 +566,21 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         if (lane < kSlabs) tma_box(sb + C::kQOff + (uint32_t)lane * C::kQSlab, &maps.q, 64 * lane, (int)s.grow, &B.q_full);
         ++tc;
         const int32_t* table = a.table + (int64_t)s.r * a.M;
-        // lane l holds the pool row of the block's run l / 2 (-1: not read), of the next block while this one's is issued
+        // lane l holds the pool row of a block's run l / 2 (-1: not read): of this block, and of the next one, which is
+        // already on its way into L2 (the ring has room for little more than one)
         auto find = [&](int b) -> int {
           const int t = s.block(b) * kBlk + (lane >> 1) * run;
-          if ((lane >> 1) >= runs || t > s.pmax || (t + run - 1 < s.lo && t >= s.snk)) return -1;
+          if (b >= s.b1 || (lane >> 1) >= runs || t > s.pmax || (t + run - 1 < s.lo && t >= s.snk)) return -1;
           return (int)pool_row(a, table, t);
         };
         int next = find(s.b0);
         for (int b = s.b0; b < s.b1; ++b, ++g) {
           const int row = next;
-          if (b + 1 < s.b1) {
-            // a block ahead into L2: the ring has room for little more than one block
-            next = find(b + 1);
-            if (next >= 0) {
+          next = find(b + 1);
+          if (next >= 0) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) tma_prefetch(&maps.pool, 128 * i + 64 * (lane & 1), next);
-              if (!(lane & 1)) tma_prefetch(&maps.pool, kVal, next);
-            }
+            for (int i = 0; i < 4; ++i) tma_prefetch(&maps.pool, 128 * i + 64 * (lane & 1), next);
+            if (!(lane & 1)) tma_prefetch(&maps.pool, kVal, next);
           }
           const uint32_t got = __popc(__ballot_sync(kFull, row >= 0)) >> 1;  // runs
           const uint32_t off = (uint32_t)((lane >> 1) * run) * 128u;
@@ -1096,38 +1095,64 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
 // row and meet in shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kJoinGroups = 4;
-constexpr int kJoinThreads = kJoinGroups * kVal / 4;
+constexpr int kJoinRow = kVal / 4;  // threads of a row
+constexpr int kJoinThreads = kJoinGroups * kJoinRow;
+constexpr int kJoinParts = 256;     // parts of a row whose weights are held at a time
 
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArgs a, float bias) {
-  __shared__ float4 acc[kJoinGroups][kVal / 4];
-  __shared__ float sum[kJoinGroups];
+  __shared__ float4 acc[kJoinGroups][kJoinRow];
+  __shared__ float weight[kJoinGroups][kJoinParts];
+  __shared__ float part_m[kJoinGroups][kJoinRow / 32], part_l[kJoinGroups][kJoinRow / 32];
   grid_wait();
   if (a.head[kHdListed] == 0) return;
-  const int group = (int)threadIdx.x / (kVal / 4), col = threadIdx.x % (kVal / 4);
+  const int group = (int)threadIdx.x / kJoinRow, col = threadIdx.x % kJoinRow, lane = threadIdx.x & 31, warp = col >> 5;
   const int items = a.head[kHdShared] * N;
   const int groups = items >= kJoinGroups * (int)gridDim.x ? 1 : kJoinGroups;  // that work on one row
   const int per_cta = kJoinGroups / groups;
   for (int first = (int)blockIdx.x * per_cta; first < items; first += (int)gridDim.x * per_cta) {
-    const int item = min(first + (per_cta > 1 ? group : 0), items - 1), row = item % N;
+    const int mine = first + (per_cta > 1 ? group : 0);
+    const int item = min(mine, items - 1), row = item % N;
     const int4 sh = a.shared[item / N];  // tile, first CTA, last CTA, slot of the first one's part (0 for the others)
     const int4 d = a.tiles[sh.x];
     Seg s;
     tile_of(a, N, d.x, d.y, s);
-    const bool in = row < s.nrows && first + (per_cta > 1 ? group : 0) < items;
-    auto part = [&](int w) -> int64_t { return (int64_t)w * 2 + (w == sh.y ? sh.w : 0); };
-    float m = kNone;
+    const bool in = row < s.nrows && mine < items;
+    const int n = sh.z - sh.y + 1;  // at most the CTAs of the launch
+    auto part = [&](int k) -> int64_t { return (int64_t)(sh.y + k) * 2 + (k == 0 ? sh.w : 0); };
+    // each group holds the weight of every part of its row: 2^(m - largest m), and their sum of l
+    float mk[kJoinParts / kJoinRow], lk[kJoinParts / kJoinRow], m = kNone, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinParts / kJoinRow; ++k) {
+      const int i = col + k * kJoinRow;
+      const float* ml = a.part_ml + part(i) * 2 * N + row;
+      mk[k] = in && i < n ? ml[0] : kNone;
+      lk[k] = in && i < n ? ml[N] : 0.f;
+      m = fmaxf(m, mk[k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if (lane == 0) part_m[group][warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoinRow / 32; ++k) m = fmaxf(m, part_m[group][k]);
+#pragma unroll
+    for (int k = 0; k < kJoinParts / kJoinRow; ++k) {
+      const float f = ex2(mk[k] - m);
+      weight[group][col + k * kJoinRow] = f;
+      l += f * lk[k];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+    if (lane == 0) part_l[group][warp] = l;
+    __syncthreads();
+    l = (part_l[group][0] + part_l[group][1]) + (part_l[group][2] + part_l[group][3]);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
     if (in) {
 #pragma unroll 8
-      for (int w = sh.y; w <= sh.z; ++w) m = fmaxf(m, a.part_ml[part(w) * 2 * N + row]);
-#pragma unroll 8
-      for (int w = sh.y + (groups > 1 ? group : 0); w <= sh.z; w += groups) {
-        const int64_t p = part(w);
-        const float4 y = reinterpret_cast<const float4*>(a.part_o + (p * N + row) * kVal)[col];
-        const float f = ex2(a.part_ml[p * 2 * N + row] - m);
-        l += f * a.part_ml[p * 2 * N + N + row];
+      for (int k = groups > 1 ? group : 0; k < n; k += groups) {
+        const float4 y = reinterpret_cast<const float4*>(a.part_o + (part(k) * N + row) * kVal)[col];
+        const float f = weight[group][k];
         x.x += f * y.x;
         x.y += f * y.y;
         x.z += f * y.z;
@@ -1135,9 +1160,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArg
       }
     }
     if (groups > 1) {
-      __syncthreads();  // the last row's sums have been read
       acc[group][col] = x;
-      if (col == 0) sum[group] = l;
       __syncthreads();
       if (group == 0) {
 #pragma unroll
@@ -1147,7 +1170,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArg
           x.y += y.y;
           x.z += y.z;
           x.w += y.w;
-          l += sum[k];
         }
       }
     }
@@ -1158,6 +1180,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArg
           make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
       if (col == 0 && a.lse) a.lse[s.grow + row] = l == 0.f ? -INFINITY : (m - bias + log2f(l)) * 0.6931471805599453f;
     }
+    __syncthreads();  // the next row's weights take this one's place
   }
 }
 
@@ -1208,9 +1231,16 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, size_t sme
 template <int N, bool kQ4>
 cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
   using C = Shape<N, kQ4>;
+  static_assert(kMaxWorkers <= kJoinParts, "parts of a tile");
   if (a.n_tokens == 0) return cudaMemsetAsync(a.status, 0, 4, s);
-  cudaError_t e = cudaFuncSetAttribute(attend_paged_kernel<N, kQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  static std::atomic<uint64_t> ready{0};  // devices where the kernel may have its shared memory
+  const uint64_t bit = a.device < 64 ? 1ull << a.device : 0ull;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(attend_paged_kernel<N, kQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   Maps maps{};
   if (!kQ4) {
     maps.run = a.B & -a.B;
