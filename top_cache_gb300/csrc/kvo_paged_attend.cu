@@ -76,7 +76,6 @@ constexpr uint32_t kSlab = kBlk * 128;       // bytes of one slab of a block
 constexpr uint32_t kPair = 2 * kSlab;
 constexpr int kMaxRing = 5;
 constexpr float kNone = -3.0e38f;            // running maximum before any visible token
-constexpr float kRescale = 8.f;              // log2: how far a score may pass the running maximum
 
 template <int N, bool kQ4>
 struct Shape {
@@ -101,7 +100,11 @@ struct Shape {
   static constexpr uint32_t kSmem = kBarOff + 256 + 1024;  // barriers and flags, alignment slack
   static constexpr uint32_t kTmem = N == 64 ? 512 : N == 32 ? 256 : 128;
   static constexpr uint32_t kColS = 4 * N;             // O^T: value elements 128 i.. at columns i * N
+  static constexpr bool kAhead = !kQ4;                 // softmax holds the next tile beside this one (registers)
   static constexpr float kBias = kQ4 ? 7.f : 0.f;      // P is 2^kBias exp2(..): keeps small weights out of fp16's subnormals
+  // log2: how far a score may pass the running maximum.  bf16 weights are as exact at any size, and 2^40 of them
+  // stay far from fp32's range; fp16 ends at 2^16.
+  static constexpr float kRescale = kQ4 ? 8.f : 40.f;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
   static_assert(kRingOff % 1024 == 0 && kPOff % 1024 == 0 && kMiscOff % 16 == 0 && kBarOff % 8 == 0,
                 "swizzled tiles sit on 1 KB boundaries");
@@ -221,6 +224,11 @@ __device__ __forceinline__ bool named_any(uint32_t id, uint32_t threads, bool p)
       : "memory");
   return r != 0;
 }
+// Bits whose order as integers is the values' (its own inverse); a positive NaN above all.
+__device__ __forceinline__ int32_t as_ordered(float x) {
+  const int32_t b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
 // 2^x, hardware approximation (relative error near 2^-22); 2^-inf = 0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -236,44 +244,43 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 // One tile, or the part of its blocks that this CTA has.
 struct Seg {
   int r;                 // request
-  int64_t grow;          // first row of the tile among all (token, head) rows
+  int grow;              // first row of the tile among all (token, head) rows
   int row0, nrows;       // first row within the request, rows
-  int pos0, H;           // position of the request's first query token, heads
+  int pos0;              // position of the request's first query token
   int pmin, pmax;        // positions of the tile's first and last row
-  int lo, snk;           // window part starts here; tokens below snk are seen by all positions at or past them
-  int wlo, nsb, nblk;    // first block of the window part, blocks of the sinks before it, blocks
-  int b0, b1;            // this CTA's blocks of the list
+  int lo;                // window part starts here; tokens below a.sinks are seen by all positions at or past them
+  int wlo, nsb;          // first block of the window part, blocks of the sinks before it
+  int b0, b1;            // this CTA's blocks of the tile's list
   int part;              // -1: whole tile, else its partial slot
   __device__ __forceinline__ int block(int b) const { return b < nsb ? b : wlo + (b - nsb); }
-  __device__ __forceinline__ bool any_sees(int t) const { return t <= pmax && (t >= lo || t < snk); }
+  __device__ __forceinline__ bool any_sees(const PagedAttendArgs& a, int t) const {
+    return t <= pmax && (t >= lo || t < a.sinks);
+  }
 };
 
-__device__ __forceinline__ void tile_of(const PagedAttendArgs& a, int N, int r, int row0, Seg& s) {
+// Fills all but the CTA's share; returns the tile's blocks.
+__device__ __forceinline__ int tile_of(const PagedAttendArgs& a, int N, int r, int row0, Seg& s) {
   const int c0 = min(max(a.cu[r], 0), a.n_tokens), c1 = min(max(a.cu[r + 1], c0), a.n_tokens);
   const int nq = c1 - c0;
   const int kv = (int)min((int64_t)max(a.kv_lens[r], 0), (int64_t)a.M * a.B);
   s.r = r;
-  s.H = a.H;
   s.row0 = row0;
   s.nrows = min(N, nq * a.H - row0);
-  s.grow = (int64_t)c0 * a.H + row0;
+  s.grow = c0 * a.H + row0;
   s.pos0 = kv - nq;
   s.pmin = s.pos0 + row0 / a.H;
   s.pmax = s.pos0 + (row0 + s.nrows - 1) / a.H;
   s.lo = a.window > 0 ? max(0, s.pmin - a.window + 1) : 0;
-  s.snk = a.sinks;
   s.wlo = 0;
   s.nsb = 0;
-  s.nblk = 0;
-  if (s.pmax >= 0) {
-    const int nsb = (min(a.sinks, s.pmax + 1) + kBlk - 1) / kBlk;
-    const int wlo = s.lo / kBlk;
-    if (nsb < wlo) {
-      s.nsb = nsb;
-      s.wlo = wlo;
-    }
-    s.nblk = s.nsb + s.pmax / kBlk - s.wlo + 1;
+  if (s.pmax < 0) return 0;
+  const int nsb = (min(a.sinks, s.pmax + 1) + kBlk - 1) / kBlk;
+  const int wlo = s.lo / kBlk;
+  if (nsb < wlo) {
+    s.nsb = nsb;
+    s.wlo = wlo;
   }
+  return s.nsb + s.pmax / kBlk - s.wlo + 1;
 }
 __device__ __forceinline__ int request_rows(const PagedAttendArgs& a, int r) {
   const int c0 = min(max(a.cu[r], 0), a.n_tokens), c1 = min(max(a.cu[r + 1], c0), a.n_tokens);
@@ -317,24 +324,23 @@ struct Walk {
         hi = min(lo + (below + 1) * step, hi);
         lo = lo + below * step;
       }
-      tile_of(a, N, lo, (tile - a.tile_off[lo]) * N, s);
+      s.b1 = tile_of(a, N, lo, (tile - a.tile_off[lo]) * N, s);
       s.b0 = 0;
-      s.b1 = s.nblk;
       s.part = -1;
       tile += (int)gridDim.x;
       return true;
     }
     while (tile < end_tile || (tile == end_tile && unit < end_unit)) {
       const int4 d = a.tiles[tile];
-      tile_of(a, N, d.x, d.y, s);
-      const int last = tile == end_tile ? end_unit : s.nblk + kTileCost;
+      const int nblk = tile_of(a, N, d.x, d.y, s);
+      const int last = tile == end_tile ? end_unit : nblk + kTileCost;
       s.b0 = max(unit - kTileCost, 0);
       s.b1 = max(last - kTileCost, 0);
       const bool first = unit < kTileCost;  // has the tile's own unit
-      s.part = s.b0 == 0 && s.b1 == s.nblk ? -1 : (first ? 1 : 0);
+      s.part = s.b0 == 0 && s.b1 == nblk ? -1 : (first ? 1 : 0);
       ++tile;
       unit = 0;
-      if (s.b0 < s.b1 || (s.nblk == 0 && first)) return true;
+      if (s.b0 < s.b1 || (nblk == 0 && first)) return true;
     }
     return false;
   }
@@ -380,10 +386,10 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAtte
     if (i < n_tiles) {
       const int r = segment_of(off, a.R, i);
       Seg s;
-      tile_of(a, N, r, (i - off[r]) * N, s);
-      cost[k] = s.nblk + kTileCost;
+      const int nblk = tile_of(a, N, r, (i - off[r]) * N, s);
+      cost[k] = nblk + kTileCost;
       atomicMax(&most, cost[k]);
-      a.tiles[i] = make_int4(r, s.row0, s.nblk, 0);
+      a.tiles[i] = make_int4(r, s.row0, nblk, 0);
     }
   }
   // at most 2048 tiles of at most 2^23 + 1 units: the sum can pass 2^31, and is then cut off (the shares only get uneven)
@@ -563,14 +569,14 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&B.q_full, kSlabs * C::kQSlab);
         __syncwarp();
         // rows behind the tile's are the next ones' or zeros, and go nowhere
-        if (lane < kSlabs) tma_box(sb + C::kQOff + (uint32_t)lane * C::kQSlab, &maps.q, 64 * lane, (int)s.grow, &B.q_full);
+        if (lane < kSlabs) tma_box(sb + C::kQOff + (uint32_t)lane * C::kQSlab, &maps.q, 64 * lane, s.grow, &B.q_full);
         ++tc;
         const int32_t* table = a.table + (int64_t)s.r * a.M;
         // lane l holds the pool row of a block's run l / 2 (-1: not read): of this block, and of the next one, which is
         // already on its way into L2 (the ring has room for little more than one)
         auto find = [&](int b) -> int {
           const int t = s.block(b) * kBlk + (lane >> 1) * run;
-          if (b >= s.b1 || (lane >> 1) >= runs || t > s.pmax || (t + run - 1 < s.lo && t >= s.snk)) return -1;
+          if (b >= s.b1 || (lane >> 1) >= runs || t > s.pmax || (t + run - 1 < s.lo && t >= a.sinks)) return -1;
           return (int)pool_row(a, table, t);
         };
         int next = find(s.b0);
@@ -635,7 +641,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         }
         const int t = fs.block(fb) * kBlk + tok, j = entry_of(a, t);
         f_in = t - j * a.B;
-        f_entry = fs.any_sees(t) ? __ldg(a.table + (int64_t)fs.r * a.M + j) : -1;
+        f_entry = fs.any_sees(a, t) ? __ldg(a.table + (int64_t)fs.r * a.M + j) : -1;
       };
       const uint8_t *crow = nullptr, *srow = nullptr;  // null: zeros
       auto locate = [&]() {
@@ -679,7 +685,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         if (tc >= 1 && !wait(&B.q_free, (uint32_t)(tc - 1))) { ok = false; break; }
         // queries: one warp per row; scaled by 2^-e so that the largest magnitude is in [2^14, 2^15)
         for (int r = warp - kProd0; r < N; r += C::kProdWarps) {
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + (s.grow + r) * kRow);
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(s.grow + r) * kRow);
           uint4 v[3];
           uint32_t top = 0u;
 #pragma unroll
@@ -844,10 +850,15 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       return *f == 0u;
     };
     bool ok = true, any;
-    while (ok && walk.next(a, s)) {
+    // kAhead: the next tile is looked up behind the first block's weights, when these warps have time
+    Seg after;
+    bool more = walk.next(a, after);
+    while (ok && more) {
+      s = after;
       if (s.b0 >= s.b1) {  // nothing visible
+        more = walk.next(a, after);
         for (int i = st; i < s.nrows * (kVal / 8); i += kSoftThreads)
-          reinterpret_cast<uint4*>(a.out + s.grow * kVal)[i] = make_uint4(0u, 0u, 0u, 0u);
+          reinterpret_cast<uint4*>(a.out + (int64_t)s.grow * kVal)[i] = make_uint4(0u, 0u, 0u, 0u);
         if (a.lse && st < s.nrows) a.lse[s.grow + st] = -INFINITY;
         continue;
       }
@@ -856,7 +867,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       const float* qm = q_mul + (tc & 1) * N;
       if (quad == 0 && lane < NC) {
         lm[c0 + lane] = C::kBias - kNone;
-        pos[c0 + lane] = s.pos0 + (s.row0 + min(c0 + lane, s.nrows - 1)) / s.H;
+        pos[c0 + lane] = s.pos0 + (s.row0 + min(c0 + lane, s.nrows - 1)) / a.H;
       }
       if (kQ4) {  // the factors; the next tile's queries may not be announced before both halves have seen these
         dead = dead || !wait(&B.q_full, (uint32_t)tc);
@@ -869,7 +880,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       for (int c = 0; c < NC; ++c) l[c] = 0.f;
       auto mapped = [&](int b) -> bool {
         const int t = s.block(b) * kBlk + tok;
-        return b < s.b1 && s.any_sees(t) && pool_row(a, table, t) >= 0;
+        return b < s.b1 && s.any_sees(a, t) && pool_row(a, table, t) >= 0;
       };
       bool here_next = mapped(s.b0);
       for (int b = s.b0; b < s.b1; ++b, ++g) {
@@ -877,12 +888,12 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         here_next = mapped(b + 1);
         const int t = s.block(b) * kBlk + tok;
         // the token is seen by every position of the tile, or by some
-        const bool all = here && t <= s.pmin && (a.window == 0 || t > s.pmax - a.window || t < s.snk);
+        const bool all = here && t <= s.pmin && (a.window == 0 || t > s.pmax - a.window || t < a.sinks);
         const bool plain = __all_sync(kFull, all);
         // bit c: row c0 + c sees the token.  Position p sees token t when p - t is in [0, span).
         uint32_t vis = kFull;
         if (!plain) {
-          const uint32_t span = !here ? 0u : (a.window == 0 || t < s.snk) ? 0x7fffffffu : (uint32_t)a.window;
+          const uint32_t span = !here ? 0u : (a.window == 0 || t < a.sinks) ? 0x7fffffffu : (uint32_t)a.window;
           vis = 0u;
 #pragma unroll
           for (int c = 0; c < NC; c += 4) {
@@ -927,17 +938,19 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         float top = v[0];
 #pragma unroll
         for (int c = 1; c < NC; ++c) top = fmaxf(top, v[c]);
-        if (!meet(b == s.b0 || top > kRescale + C::kBias, any)) { ok = false; break; }
+        if (!meet(b == s.b0 || top > C::kRescale + C::kBias, any)) { ok = false; break; }
         if (any) {
           // the tokens' maximum of each row; then the running maximum, the sums and O^T move to it
           tmem_ld<NC>(sS, v);
           tmem_wait_ld();
+          int32_t mine = 0;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const float x = (vis >> c) & 1u ? __fmul_rn(v[c], kQ4 ? qm[c0 + c] : a.scale_log2) : -INFINITY;
-            const uint32_t w = __reduce_max_sync(kFull, order_bits(fmaxf(x, -INFINITY)));  // NaN: -inf
-            if (lane == 0) warp_max[warp * NC + c] = unorder_bits(w);
+            const int32_t w = __reduce_max_sync(kFull, as_ordered(x));
+            if (lane == c) mine = w;
           }
+          if (lane < NC) warp_max[warp * NC + lane] = __int_as_float(as_ordered(__int_as_float(mine)));
           named_sync(bar_half, 128);
           if (quad == 0 && lane < NC) {
             const float* wm = warp_max + 4 * hw * NC + lane;
@@ -953,15 +966,18 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
             // s_full came after every earlier MMA, so O^T is at rest
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
-#pragma unroll 1
-              for (int c = 0; c < NC; c += 8) {
-                float o[8];
-                tmem_ld8(tmem + lane_addr + (uint32_t)(i * N + c0 + c), o);
-                tmem_wait_ld();
+              tmem_ld<NC>(tmem + lane_addr + (uint32_t)(i * N + c0), v);
+              tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] *= move_by[c0 + c + k];
-                tmem_st8(tmem + lane_addr + (uint32_t)(i * N + c0 + c), o);
+              for (int c = 0; c < NC; c += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(move_by + c0 + c);
+                v[c] *= y.x;
+                v[c + 1] *= y.y;
+                v[c + 2] *= y.z;
+                v[c + 3] *= y.w;
               }
+#pragma unroll
+              for (int c = 0; c < NC; c += 8) tmem_st8(tmem + lane_addr + (uint32_t)(i * N + c0 + c), v + c);
             }
             tmem_wait_st();
           }
@@ -1021,15 +1037,23 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         }
         tc_before();
         mbar_arrive(&B.p_full);
+        if (C::kAhead && b == s.b0) more = walk.next(a, after);
       }
       if (!ok) break;
-      // sums over the tokens of each row
+      // sums over the tokens of each row: halves of the rows change lanes until a lane has one (row lane mod NC)
+      {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float x = l[c];
+        for (int o = NC / 2; o > 0; o >>= 1) {
+          const bool up = (lane & o) != 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-        if (lane == 0) warp_sum[warp * NC + c] = x;
+          for (int c = 0; c < o; ++c) {
+            const float give = up ? l[c] : l[c + o], keep = up ? l[c + o] : l[c];
+            l[c] = keep + __shfl_xor_sync(kFull, give, o);
+          }
+        }
+#pragma unroll
+        for (int o = NC; o < 32; o <<= 1) l[0] += __shfl_xor_sync(kFull, l[0], o);
+        if (lane < NC) warp_sum[warp * NC + lane] = l[0];
       }
       named_sync(bar_half, 128);
       if (quad == 0 && lane < NC) {
@@ -1061,7 +1085,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
             if (c0 + c < s.nrows) dst[(size_t)c * kVal] = o[c];
         } else {
           // lanes 2 k and 2 k + 1 trade elements so that each stores a pair: the even one of row c, the odd one of c + 1
-          uint16_t* dst = a.out + (s.grow + c0) * kVal + (e & ~1);
+          uint16_t* dst = a.out + (int64_t)(s.grow + c0) * kVal + (e & ~1);
           const bool odd = lane & 1;
 #pragma unroll
           for (int c = 0; c < NC; c += 2) {
@@ -1076,6 +1100,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       tc_before();
       mbar_arrive(&B.o_free);
       ++tc;
+      if (!C::kAhead) more = walk.next(a, after);
     }
     if (!ok || dead) fail();
   }
@@ -1176,7 +1201,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArg
     if (in && (groups == 1 || group == 0)) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const __nv_bfloat162 h0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), h1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-      reinterpret_cast<uint2*>(a.out + (s.grow + row) * kVal)[col] =
+      reinterpret_cast<uint2*>(a.out + (int64_t)(s.grow + row) * kVal)[col] =
           make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
       if (col == 0 && a.lse) a.lse[s.grow + row] = l == 0.f ? -INFINITY : (m - bias + log2f(l)) * 0.6931471805599453f;
     }
