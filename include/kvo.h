@@ -536,7 +536,8 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
  *                 device; 0 on a bad argument); no initialisation, not
  *                 preserved; one per call in flight
  *   status      : device uint32, nullable: set to 0, then nonzero if a bounded
- *                 wait expired (the outputs are then not valid)
+ *                 wait expired (KVO_SELECT_ERR_TIMEOUT) or cu_tokens decreases
+ *                 (KVO_SELECT_ERR_PLAN); the outputs are then not valid
  * Precision: scores and sums in fp32 on exact products; the softmax weights of
  * the value product are rounded to bf16 (KVO_CACHE_Q4: fp16), their sum is not;
  * out is rounded to bf16.  The same inputs give the same bits.

@@ -483,3 +483,19 @@ def test_a_serving_loop_in_one_graph(fmt):
                 assert np.all(np.abs(gl[a:b] - rl) <= 4 * es + 2.0 ** -20 * (1 + np.abs(rl)))
         plan = {k: want[k] for k in plan}
     assert int(plan["bounds"][1]) > 2 * n_blocks  # blocks were given back and taken again
+
+
+def test_tokens_that_decrease_are_reported():
+    # cu_tokens 0, 3, 0, 3 lists six tokens of three: nothing is read past the queries, and the status says so
+    c = Cache([9, 9, 9], 8, BF16, 22)
+    q = torch.zeros(3, 4, 576, dtype=torch.int16, device="cuda")
+    out = torch.full((3, 4, 512), 0x1234, dtype=torch.int16, device="cuda")
+    for R, cu in ((3, [0, 3, 0, 3]), (300, [0, 3] * 150 + [0])):
+        n = torch.full((R,), 9, dtype=torch.int32, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        table = _dev(np.resize(c.table, (R, c.M)))
+        K.kvo_paged_attend(c.pool, c.n_blocks, 8, BF16, table, n, _dev(cu), q, SCALE, out, status=status)
+        torch.cuda.synchronize()
+        rows = sum(max(0, b - a) for a, b in zip(cu, cu[1:])) * 4
+        many = sum(-(-max(0, b - a) * 4 // 16) for a, b in zip(cu, cu[1:])) > -(-3 * 4 // 16) + R
+        assert rows > 3 * 4 and (status.item() == 2) == many

@@ -110,6 +110,7 @@ struct PagedAttendArgs {
   uint64_t wait_ns;
   int32_t workers;         // CTAs of the attention launch
   int32_t device;
+  bool own_list;           // each CTA lists the tiles for itself
   // workspace
   int32_t* head;           // listed, tiles, CTAs in use, shared tiles
   int32_t* tile_off;       // [R + 1] tiles before each request
