@@ -482,14 +482,16 @@ int64_t kvo_paged_block_bytes(int32_t format, int32_t block_tokens);
  *   cu_new      : device int32 [n_requests + 1]: new tokens before each request
  *                 (refused ones count: they are the caller's layout)
  *   slots       : device int32 [n_slots]: slot of every new token, requests in
- *                 order; -1 for refused ones and behind the last
+ *                 order; -1 for refused ones, behind the last, and where the
+ *                 block id is negative or its slot passes 2^31 - 1
  *   status      : device int32 [n_requests]: KVO_OK; KVO_ERANGE: the length is
  *                 negative or passes max_blocks * block_tokens, or the tokens
  *                 pass n_slots; KVO_ECAPACITY: the request needs blocks and
  *                 those that requests 0..r need are more than the free ones.
  *                 A refused request changes nothing.
- * Lengths of the next call are this call's lengths_out.  An unlisted block id
- * in the ring is not checked here (kvo_paged_write and _attend do).
+ * Lengths of the next call are this call's lengths_out.  Whether a block id in
+ * the ring is one of the pool's is checked by kvo_paged_write and _attend, which
+ * skip rows past it; an id that is free twice is the caller's mistake.
  * Errors: KVO_EINVAL, KVO_ECUDA.
  */
 int kvo_paged_plan(const int32_t* lengths, const int32_t* new_tokens, int32_t n_requests,

@@ -62,7 +62,8 @@ def plan(lengths, new, block, table, ring, bounds, n_slots, window=0, sinks=0):
             released += [int(table[r, j]) for j in range(want) if j in hidden(L + n) and j not in hidden(L)]
             out["lengths"][r] = out["kv_lens"][r] = L + n
         for i in range(n):
-            out["slots"][begin + i] = table[r, (L + i) // block] * block + (L + i) % block
+            b = int(table[r, (L + i) // block])
+            out["slots"][begin + i] = b * block + (L + i) % block if 0 <= b and b * block + block <= 2 ** 31 else -1
     for i, b in enumerate(released):
         ring[(tail + i) % F] = b
     return dict(out, table=table, ring=ring, bounds=np.array([head + taken, tail + len(released)], np.int64))

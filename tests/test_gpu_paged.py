@@ -485,6 +485,115 @@ def test_a_serving_loop_in_one_graph(fmt):
     assert int(plan["bounds"][1]) > 2 * n_blocks  # blocks were given back and taken again
 
 
+def test_plan_bad_block_ids_give_no_slot():
+    ring = np.array([-3, 2 ** 31 - 1, 1 << 28, 5], np.int32)
+    args = (np.array([0, 0, 0, 0], np.int32), np.array([2, 2, 2, 2]), 8, np.full((4, 1), -1, np.int32), ring,
+            np.array([0, 4], np.int64), 9)
+    got = _run_plan(*args, 0, 0)
+    _same(got, O.plan(*args))
+    assert got["slots"].tolist() == [-1] * 6 + [40, 41, -1]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rows_past_32_bit_offsets(fmt):
+    # a pool of more than 4 GB: blocks at its far end
+    B = 4096
+    n_blocks = (5 << 30) // K.kvo_paged_block_bytes(fmt, B)
+    pool = torch.empty(n_blocks, K.kvo_paged_block_bytes(fmt, B), dtype=torch.uint8, device="cuda")
+    L = 300
+    bits = O.bf16_bits(np.random.default_rng(23).standard_normal((L, 576)))
+    slots = (n_blocks - 1) * B + np.arange(L)
+    K.kvo_paged_write(_dev(bits.view(np.int16), torch.int16), _dev(slots), pool, n_blocks, B, fmt)
+    back = torch.zeros(L, 576, dtype=torch.int16, device="cuda")
+    K.kvo_paged_read(pool, n_blocks, B, fmt, _dev(slots), back)
+    torch.cuda.synchronize()
+    rows = O.bf16_values(back.cpu().numpy().view(np.uint16))
+    assert np.array_equal(rows, O.bf16_values(bits) if fmt == BF16 else O.dequantize(*O.quantize(bits)))
+
+    class C:
+        pass
+    c = C()
+    c.pool, c.n_blocks, c.block, c.fmt, c.table, c.rows = pool, n_blocks, B, fmt, np.array([[n_blocks - 1, 7]], np.int32), rows
+    c.rows_of = lambda r: lambda t: (rows[t], np.ones(len(t), bool))
+    q = O.bf16_bits(np.random.default_rng(24).standard_normal((1, 40, 576)))
+    out, lse = _attend(c, q, [0, 1], [L], SCALE)
+    _check(c, q, [0, 1], [L], SCALE, 0, 0, out, lse)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_not_finite_beside_a_half_empty_tile(fmt):
+    # tiles of 64 rows, the last request's only 16 of them filled: the other half's rows lie past the queries
+    c = Cache([200, 90], 16, fmt, 25)
+    rows = O.bf16_bits(np.random.default_rng(26).standard_normal((2, 576)))
+    rows[0, 7], rows[1, 300] = 0x7FC0, 0x7F80
+    slots = [c.table[1, 89 // 16] * 16 + 89 % 16, c.table[0, 199 // 16] * 16 + 199 % 16]
+    K.kvo_paged_write(_dev(rows.view(np.int16), torch.int16), _dev(slots), c.pool, c.n_blocks, 16, fmt)
+    c.refresh()
+    q = O.bf16_bits(np.abs(np.random.default_rng(27).standard_normal((12, 8, 576))) + 0.1)
+    out, lse = _attend(c, q, [0, 10, 12], [200, 90], SCALE)
+    _check(c, q, [0, 10, 12], [200, 90], SCALE, 0, 0, out, lse, tokens=set(range(9)) | {10})
+    got = O.bf16_values(out)
+    assert np.isfinite(got[:9]).all() and np.isfinite(got[10]).all() and np.isnan(got[[9, 11]]).any((1, 2)).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lens,new,H", [([300, 900], [1, 2], 64), ([600] * 20, [20] * 20, 64)])
+def test_captured_call_replayed_on_new_data(fmt, lens, new, H):
+    """One call in a graph (short and long lists of tiles), replayed after lengths, table, queries and rows changed."""
+    c = Cache(lens, 32, fmt, 28)
+    g = np.random.default_rng(29)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(cu[-1])
+    q, kv, table = torch.zeros(T, H, 576, dtype=torch.int16, device="cuda"), _dev(lens), _dev(c.table)
+    out, lse = torch.zeros(T, H, 512, dtype=torch.int16, device="cuda"), torch.zeros(T, H, device="cuda")
+    cud = _dev(cu)
+
+    def call():
+        K.kvo_paged_attend(c.pool, c.n_blocks, 32, fmt, table, kv, cud, q, SCALE, out, lse)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for k in range(3):
+        bits = O.bf16_bits(g.standard_normal((T, H, 576)))
+        kv_h = [max(1, n - 31 * k) for n in lens]
+        q.copy_(_dev(bits.view(np.int16), torch.int16))
+        kv.copy_(_dev(kv_h))
+        graph.replay()
+        torch.cuda.synchronize()
+        _check(c, bits, cu, kv_h, SCALE, 0, 0, out.cpu().numpy().view(np.uint16), lse.cpu().numpy(),
+               tokens={0, 1, T // 2, T - 1})
+
+
+def test_empty_calls_and_streams():
+    c = Cache([9], 8, Q4, 30)
+    e = torch.empty(0, 576, dtype=torch.bfloat16, device="cuda")
+    s = torch.empty(0, dtype=torch.int32, device="cuda")
+    K.kvo_paged_write(e, s, c.pool, c.n_blocks, 8, Q4)
+    K.kvo_paged_read(c.pool, c.n_blocks, 8, Q4, s, e)
+    status = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    K.kvo_paged_attend(c.pool, c.n_blocks, 8, Q4, _dev(c.table), _dev([9]), _dev([0, 0]),
+                       torch.empty(0, 4, 576, dtype=torch.bfloat16, device="cuda"), SCALE,
+                       torch.empty(0, 4, 512, dtype=torch.bfloat16, device="cuda"), status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    other = torch.cuda.Stream()
+    q = torch.zeros(1, 4, 576, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(1, 4, 512, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(K.KvoError):  # a raw stream whose memory the allocator cannot order
+        K.kvo_paged_attend(c.pool, c.n_blocks, 8, Q4, _dev(c.table), _dev([9]), _dev([0, 1]), q, SCALE, out,
+                           stream=other.cuda_stream)
+    for bad in (dict(out=out[:, :2].expand(1, 2, 512)), dict(queries=q.float()), dict(kv_lens=_dev([9]).long())):
+        a = dict(block_table=_dev(c.table), kv_lens=_dev([9]), cu_tokens=_dev([0, 1]), queries=q, scale=SCALE, out=out)
+        with pytest.raises(K.KvoError) as x:
+            K.kvo_paged_attend(c.pool, c.n_blocks, 8, Q4, **{**a, **bad})
+        assert x.value.code == K.KVO_EINVAL
+    with pytest.raises(K.KvoError):
+        K.kvo_paged_write(q[0], _dev([0, 1, 2, 3]), c.pool, c.n_blocks + 1, 8, Q4)  # the pool is smaller
+
+
 def test_tokens_that_decrease_are_reported():
     # cu_tokens 0, 3, 0, 3 lists six tokens of three: nothing is read past the queries, and the status says so
     c = Cache([9, 9, 9], 8, BF16, 22)

@@ -23,7 +23,7 @@ def test_plan_refusals_change_nothing():
     r = O.plan([0, 0, 4, 0], [16, 1, 1, 17], 8, table, ring, [0, 2], 64)
     assert r["status"].tolist() == [O.OK, O.ECAPACITY, O.OK, O.ERANGE]
     assert r["lengths"].tolist() == [16, 0, 5, 0] and r["kv_lens"].tolist() == [16, 0, 5, 0]
-    assert r["slots"][16] == -1 and r["slots"][17] == -8 + 4  # (its table had no entry)
+    assert r["slots"][16:19].tolist() == [-1, -1, -1]  # refused, a table without the entry, refused
     # the slot list is too short for the second request only
     r = O.plan([0, 0, 0], [3, 9, 0], 8, np.full((3, 2), -1, np.int32), np.arange(6, dtype=np.int32), [0, 6], 8)
     assert r["status"].tolist() == [O.OK, O.ERANGE, O.OK]

