@@ -595,16 +595,14 @@ def test_empty_calls_and_streams():
 
 
 def test_tokens_that_decrease_are_reported():
-    # cu_tokens 0, 3, 0, 3 lists six tokens of three: nothing is read past the queries, and the status says so
+    # cu_tokens 0, 3, 0, 3 lists six tokens of three: nothing is computed, and the status says so
     c = Cache([9, 9, 9], 8, BF16, 22)
     q = torch.zeros(3, 4, 576, dtype=torch.int16, device="cuda")
     out = torch.full((3, 4, 512), 0x1234, dtype=torch.int16, device="cuda")
-    for R, cu in ((3, [0, 3, 0, 3]), (300, [0, 3] * 150 + [0])):
+    for R, cu in ((3, [0, 3, 0, 3]), (3, [0, 0, 3, 2]), (300, [0, 3] * 150 + [0])):
         n = torch.full((R,), 9, dtype=torch.int32, device="cuda")
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         table = _dev(np.resize(c.table, (R, c.M)))
         K.kvo_paged_attend(c.pool, c.n_blocks, 8, BF16, table, n, _dev(cu), q, SCALE, out, status=status)
         torch.cuda.synchronize()
-        rows = sum(max(0, b - a) for a, b in zip(cu, cu[1:])) * 4
-        many = sum(-(-max(0, b - a) * 4 // 16) for a, b in zip(cu, cu[1:])) > -(-3 * 4 // 16) + R
-        assert rows > 3 * 4 and (status.item() == 2) == many
+        assert status.item() == 2 and bool((out == 0x1234).all())

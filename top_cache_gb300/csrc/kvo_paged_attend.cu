@@ -320,6 +320,7 @@ struct List {
 // Tiles per request; if they are few, the units before each, and how many CTAs share them evenly (0: each tile goes to
 // one CTA whole).  kThreads threads call it; `off` holds R + 1, `before` kMost entries.  publish: what the attention and
 // the join read is written to the workspace.
+constexpr int64_t kNoList = (int64_t)1 << 32;  // counted for a request whose tokens end before they start
 template <int kThreads, int kMost>
 __device__ __forceinline__ void build_list(const PagedAttendArgs& a, int N, int32_t* off, int32_t* before, List& t,
                                            bool publish) {
@@ -328,13 +329,13 @@ __device__ __forceinline__ void build_list(const PagedAttendArgs& a, int N, int3
   if (tid == 0) t.n_shared = t.most = 0;
   for (int base = 0; base < a.R; base += kThreads) {
     const int r = base + tid;
-    const int64_t n = r < a.R ? (request_rows(a, r) + N - 1) / N : 0;
+    int64_t n = 0;
+    if (r < a.R) n = a.cu[r + 1] < a.cu[r] ? kNoList : (request_rows(a, r) + N - 1) / N;
     const int64_t at = total + block_exclusive_sum<kThreads>(n, t.warp_sums, &sum);
     if (r < a.R) off[r] = (int32_t)at;
     total += sum;
   }
-  // (tokens that decrease can list more rows than there are: nothing is done then)
-  const bool valid = total <= ((int64_t)a.n_tokens * a.H + N - 1) / N + a.R;
+  const bool valid = total < kNoList;  // (else off is not what it says, and nothing reads it)
   const int n_tiles = valid ? (int)total : 0;
   if (tid == 0) {
     off[a.R] = n_tiles;
@@ -365,19 +366,20 @@ __device__ __forceinline__ void build_list(const PagedAttendArgs& a, int N, int3
     }
     mine += cost[k];
   }
-  // at most kListTiles tiles of at most 2^23 + 1 units: the sum can pass 2^31, and is then cut off (the shares get uneven)
+  // at most kListTiles tiles of at most 2^23 + 1 units: a sum past 2^31, which `before` does not hold, is not split
   int64_t units, at = block_exclusive_sum<kThreads>(mine, t.warp_sums, &units);
   const int64_t at0 = at;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    if (kPer * tid + k < kMost) before[kPer * tid + k] = (int32_t)min(at, (int64_t)INT32_MAX);
+    if (kPer * tid + k < kMost) before[kPer * tid + k] = (int32_t)at;
     at += cost[k];
   }
   const int64_t share = max((int64_t)kMinShare, (units + a.workers - 1) / a.workers);
   const int used = (int)min((int64_t)a.workers, (units + share - 1) / share);
   __syncthreads();
   // whole tiles, if the longest of them for every round take no longer than even shares and what joining them costs
-  if ((int64_t)((n_tiles + a.workers - 1) / a.workers) * t.most <=
+  if (units > INT32_MAX ||
+      (int64_t)((n_tiles + a.workers - 1) / a.workers) * t.most <=
       (units + used - 1) / max(used, 1) + split_cost(N, used, a.workers))
     return;
   if (tid == 0) {
@@ -408,7 +410,7 @@ __device__ __forceinline__ void build_list(const PagedAttendArgs& a, int N, int3
 __device__ __forceinline__ int2 share_start(const int32_t* before, int n_tiles, int64_t units, int used, int w) {
   if (w >= used) return make_int2(n_tiles, 0);
   const int64_t u = (int64_t)w * units / used;
-  const int i = segment_of(before, n_tiles, (int)min(u, (int64_t)INT32_MAX));
+  const int i = segment_of(before, n_tiles, (int)u);
   return make_int2(i, (int)(u - before[i]));
 }
 
