@@ -114,9 +114,9 @@ struct PagedAttendArgs {
   // workspace
   int32_t* head;           // listed, tiles, CTAs in use, shared tiles
   int32_t* tile_off;       // [R + 1] tiles before each request
-  int4* tiles;             // [kListTiles] request, first row, blocks, cost before
+  int2* tiles;             // [kListTiles] request, first row
   int2* start;             // [workers + 1] tile, unit
-  int4* shared;            // [workers] tile, first and last CTA, slot of the first one's part
+  int4* shared;            // [workers] first row; 2 rows + slot of the first CTA's part; first and last CTA
   float* part_ml;          // [workers][2][2][N]
   float* part_o;           // [workers][2][N][512]
 };

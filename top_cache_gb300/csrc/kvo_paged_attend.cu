@@ -350,19 +350,21 @@ __device__ __forceinline__ void build_list(const PagedAttendArgs& a, int N, int3
   __syncthreads();
   if (n_tiles > kMost) return;
   constexpr int kPer = (kMost + kThreads - 1) / kThreads;  // tiles of a thread, side by side
-  int cost[kPer];
+  int cost[kPer], grow[kPer], nrows[kPer];
   int64_t mine = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int i = kPer * tid + k;
-    cost[k] = 0;
+    cost[k] = grow[k] = nrows[k] = 0;
     if (i < n_tiles) {
       const int r = segment_of(off, a.R, i);
       Seg s;
       const int nblk = tile_of(a, N, r, (i - off[r]) * N, s);
       cost[k] = nblk + kTileCost;
+      grow[k] = s.grow;
+      nrows[k] = s.nrows;
       atomicMax(&t.most, cost[k]);
-      if (publish) a.tiles[i] = make_int4(r, s.row0, nblk, 0);
+      if (publish) a.tiles[i] = make_int2(r, s.row0);
     }
     mine += cost[k];
   }
@@ -394,7 +396,8 @@ __device__ __forceinline__ void build_list(const PagedAttendArgs& a, int N, int3
       if (cost[k] > kTileCost) {
         const int w0 = (int)(((at + kTileCost + 1) * used - 1) / units), w1 = (int)(((at + cost[k]) * used - 1) / units);
         if (w1 > w0)
-          a.shared[atomicAdd(&t.n_shared, 1)] = make_int4(kPer * tid + k, w0, w1, (int64_t)w0 * units / used <= at ? 1 : 0);
+          a.shared[atomicAdd(&t.n_shared, 1)] =
+              make_int4(grow[k], 2 * nrows[k] + ((int64_t)w0 * units / used <= at ? 1 : 0), w0, w1);
       }
       at += cost[k];
     }
@@ -484,7 +487,7 @@ struct Walk {
         r = segment_of(t.off, a.R, tile);
         row0 = (tile - t.off[r]) * N;
       } else {
-        const int4 d = a.tiles[tile];
+        const int2 d = a.tiles[tile];
         r = d.x;
         row0 = d.y;
       }
@@ -1059,13 +1062,11 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           scores(std::false_type{});
           named_sync(bar_half, 128);  // move_by is free
         }
-        // weights; the sum keeps them in fp32
+        // weights
         uint32_t p[NC / 2];
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {
-          const float e0 = ex2(v[c]), e1 = ex2(v[c + 1]);
-          l[c] += e0;
-          l[c + 1] += e1;
+          const float e0 = v[c] = ex2(v[c]), e1 = v[c + 1] = ex2(v[c + 1]);
           if (kQ4) {
             const __half2 h = __floats2half2_rn(e0, e1);
             p[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
@@ -1112,6 +1113,10 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         }
         tc_before();
         mbar_arrive(&B.p_full);
+        // the sums keep the weights in fp32; behind the arrival, while the MMAs run (before it, 4 bits at N = 64: 121 us
+        // for 119 over one request of 256k)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) l[c] += v[c];
         if (C::kAhead && b == s.b0) more = walk.next(a, own, after);
       }
       if (!ok) break;
@@ -1189,98 +1194,108 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// join: the parts of a tile that several CTAs share, in a fixed order.  128
-// threads have a row, four value elements each.  Many rows: four rows per CTA;
-// few (one long request): the four groups of a CTA take every fourth part of one
-// row and meet in shared memory.
+// join: the parts of a tile that several CTAs share, in a fixed order.  A warp
+// has a row, or with few rows (one long request) up to eight warps do: each sums
+// every eighth part, and they meet in shared memory.  Latency bound: the list,
+// the parts' (m, l) and the parts themselves are read one after another, and the
+// kernel's code is cold.  So the loop over the parts stays short: 8,192 rows in 280
+// parts of 64, 36 MB, 5.8 us (two parts a turn 7.8, four 7.4); 512 rows 4.8 us (6.7,
+// 7.3).  A CTA of 512 threads per four rows, with the weights in shared memory,
+// took 11.5 and 8.4 us; an empty list takes 2.0.
 // ---------------------------------------------------------------------------
-constexpr int kJoinGroups = 4;
-constexpr int kJoinRow = kVal / 4;  // threads of a row
-constexpr int kJoinThreads = kJoinGroups * kJoinRow;
-constexpr int kJoinParts = 256;     // parts of a row whose weights are held at a time
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
+constexpr int kJoinParts = 256;  // most parts of a row
 
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArgs a, float bias) {
-  __shared__ float4 acc[kJoinGroups][kJoinRow];
-  __shared__ float weight[kJoinGroups][kJoinParts];
-  __shared__ float part_m[kJoinGroups][kJoinRow / 32], part_l[kJoinGroups][kJoinRow / 32];
+  __shared__ float4 acc[kJoinWarps][kVal / 4];
+  constexpr int kPer = kJoinParts / 32, kCols = kVal / 4 / 32;  // parts, float4s of a lane
   grid_wait();
   if (a.head[kHdListed] == 0) return;
-  const int group = (int)threadIdx.x / kJoinRow, col = threadIdx.x % kJoinRow, lane = threadIdx.x & 31, warp = col >> 5;
+  const int warp = (int)threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int items = a.head[kHdShared] * N;
-  const int groups = items >= kJoinGroups * (int)gridDim.x ? 1 : kJoinGroups;  // that work on one row
-  const int per_cta = kJoinGroups / groups;
-  for (int first = (int)blockIdx.x * per_cta; first < items; first += (int)gridDim.x * per_cta) {
-    const int mine = first + (per_cta > 1 ? group : 0);
-    const int item = min(mine, items - 1), row = item % N;
-    const int4 sh = a.shared[item / N];  // tile, first CTA, last CTA, slot of the first one's part (0 for the others)
-    const int4 d = a.tiles[sh.x];
-    Seg s;
-    tile_of(a, N, d.x, d.y, s);
-    const bool in = row < s.nrows && mine < items;
-    const int n = sh.z - sh.y + 1;  // at most the CTAs of the launch
-    auto part = [&](int k) -> int64_t { return (int64_t)(sh.y + k) * 2 + (k == 0 ? sh.w : 0); };
-    // each group holds the weight of every part of its row: 2^(m - largest m), and their sum of l
-    float mk[kJoinParts / kJoinRow], lk[kJoinParts / kJoinRow], m = kNone, l = 0.f;
+  int team = kJoinWarps;  // warps of a row
+  while (team > 1 && items * team > kJoinWarps * (int)gridDim.x) team >>= 1;
+  const int member = warp & (team - 1), rows = kJoinWarps / team;
+  for (int first = (int)blockIdx.x * rows; first < items; first += (int)gridDim.x * rows) {
+    const int mine = first + warp / team, item = min(mine, items - 1), row = item % N;
+    const int4 sh = a.shared[item / N];  // first row, 2 rows + slot of the first CTA's part (0 for the others), CTAs
+    const bool in = row < (sh.y >> 1) && mine < items;
+    const int n = in ? sh.w - sh.z + 1 : 0;  // at most the CTAs of the launch
+    auto slot = [&](int k) -> int64_t { return (int64_t)(sh.z + k) * 2 + (k == 0 ? sh.y & 1 : 0); };
+    // the weight of every part: 2^(m - largest m), and the sum of their l
+    float f[kPer], g[kPer], m = kNone, l = 0.f;
 #pragma unroll
-    for (int k = 0; k < kJoinParts / kJoinRow; ++k) {
-      const int i = col + k * kJoinRow;
-      const float* ml = a.part_ml + part(i) * 2 * N + row;
-      mk[k] = in && i < n ? ml[0] : kNone;
-      lk[k] = in && i < n ? ml[N] : 0.f;
-      m = fmaxf(m, mk[k]);
+    for (int j = 0; j < kPer; ++j) {
+      const int k = 32 * j + lane;
+      f[j] = kNone;
+      g[j] = 0.f;
+      if (k < n) {
+        const float* ml = a.part_ml + slot(k) * 2 * N + row;
+        f[j] = ml[0];
+        g[j] = ml[N];
+      }
+      m = fmaxf(m, f[j]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    if (lane == 0) part_m[group][warp] = m;
-    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kJoinRow / 32; ++k) m = fmaxf(m, part_m[group][k]);
-#pragma unroll
-    for (int k = 0; k < kJoinParts / kJoinRow; ++k) {
-      const float f = ex2(mk[k] - m);
-      weight[group][col + k * kJoinRow] = f;
-      l += f * lk[k];
+    for (int j = 0; j < kPer; ++j) {
+      f[j] = ex2(f[j] - m);
+      l += f[j] * g[j];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-    if (lane == 0) part_l[group][warp] = l;
-    __syncthreads();
-    l = (part_l[group][0] + part_l[group][1]) + (part_l[group][2] + part_l[group][3]);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (in) {
-#pragma unroll 8
-      for (int k = groups > 1 ? group : 0; k < n; k += groups) {
-        const float4 y = reinterpret_cast<const float4*>(a.part_o + (part(k) * N + row) * kVal)[col];
-        const float f = weight[group][k];
-        x.x += f * y.x;
-        x.y += f * y.y;
-        x.z += f * y.z;
-        x.w += f * y.w;
-      }
-    }
-    if (groups > 1) {
-      acc[group][col] = x;
-      __syncthreads();
-      if (group == 0) {
+    float4 x[kCols];
 #pragma unroll
-        for (int k = 1; k < kJoinGroups; ++k) {
-          const float4 y = acc[k][col];
-          x.x += y.x;
-          x.y += y.y;
-          x.z += y.z;
-          x.w += y.w;
+    for (int c = 0; c < kCols; ++c) x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int end = min(32, n - 32 * j);
+#pragma unroll 1
+      for (int k = member; k < end; k += team) {
+        const float4* src = reinterpret_cast<const float4*>(a.part_o + (slot(32 * j + k) * N + row) * kVal) + lane;
+        const float w = __shfl_sync(kFull, f[j], k);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const float4 y = src[32 * c];
+          x[c].x += w * y.x;
+          x[c].y += w * y.y;
+          x[c].z += w * y.z;
+          x[c].w += w * y.w;
         }
       }
     }
-    if (in && (groups == 1 || group == 0)) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const __nv_bfloat162 h0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), h1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-      reinterpret_cast<uint2*>(a.out + (int64_t)(s.grow + row) * kVal)[col] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-      if (col == 0 && a.lse) a.lse[s.grow + row] = l == 0.f ? -INFINITY : (m - bias + log2f(l)) * 0.6931471805599453f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint2* out = reinterpret_cast<uint2*>(a.out + ((int64_t)sh.x + row) * kVal);
+    auto store = [&](int col, float4 y) {
+      const __nv_bfloat162 h0 = __floats2bfloat162_rn(y.x * inv, y.y * inv), h1 = __floats2bfloat162_rn(y.z * inv, y.w * inv);
+      out[col] = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+    };
+    if (in && a.lse && member == 0 && lane == 0)
+      a.lse[sh.x + row] = l == 0.f ? -INFINITY : (m - bias + log2f(l)) * 0.6931471805599453f;
+    if (team == 1) {
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+        if (in) store(32 * c + lane, x[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[warp][32 * c + lane] = x[c];
+      __syncthreads();
+      for (int col = 32 * member + lane; in && col < kVal / 4; col += 32 * team) {
+        float4 y = acc[warp - member][col];
+        for (int k = 1; k < team; ++k) {
+          const float4 z = acc[warp - member + k][col];
+          y.x += z.x;
+          y.y += z.y;
+          y.z += z.z;
+          y.w += z.w;
+        }
+        store(col, y);
+      }
+      __syncthreads();  // the next rows take these ones' place
     }
-    __syncthreads();  // the next row's weights take this one's place
   }
 }
 
@@ -1372,8 +1387,8 @@ int paged_tile_rows(int n_requests, int n_tokens, int H) {
 }
 size_t paged_attend_workspace(int n_requests, int n_tokens, int H, int workers) {
   const size_t N = (size_t)paged_tile_rows(n_requests, n_tokens, H), W = (size_t)workers;
-  return 256 + up256(((size_t)n_requests + 1) * 4) + up256(kListTiles * sizeof(int4)) + up256((W + 1) * sizeof(int2)) +
-         up256(W * sizeof(int4)) +          up256(W * 4 * N * 4) + W * 2 * N * kVal * 4;
+  return 256 + up256(((size_t)n_requests + 1) * 4) + up256(kListTiles * sizeof(int2)) + up256((W + 1) * sizeof(int2)) +
+         up256(W * sizeof(int4)) + up256(W * 4 * N * 4) + W * 2 * N * kVal * 4;
 }
 void paged_attend_carve(PagedAttendArgs& a, uint8_t* w) {
   const size_t N = (size_t)paged_tile_rows(a.R, a.n_tokens, a.H), W = (size_t)a.workers;
@@ -1382,8 +1397,8 @@ void paged_attend_carve(PagedAttendArgs& a, uint8_t* w) {
   w += 256;
   a.tile_off = reinterpret_cast<int32_t*>(w);
   w += up256(((size_t)a.R + 1) * 4);
-  a.tiles = reinterpret_cast<int4*>(w);
-  w += up256(kListTiles * sizeof(int4));
+  a.tiles = reinterpret_cast<int2*>(w);
+  w += up256(kListTiles * sizeof(int2));
   a.start = reinterpret_cast<int2*>(w);
   w += up256((W + 1) * sizeof(int2));
   a.shared = reinterpret_cast<int4*>(w);
