@@ -110,7 +110,7 @@ struct PagedAttendArgs {
   uint64_t wait_ns;
   int32_t workers;         // CTAs of the attention launch
   int32_t device;
-  bool own_list;           // each CTA lists the tiles for itself
+  bool few_tiles, own_list;  // the list is short; each CTA makes it for itself
   // workspace
   int32_t* head;           // listed, tiles, CTAs in use, shared tiles
   int32_t* tile_off;       // [R + 1] tiles before each request

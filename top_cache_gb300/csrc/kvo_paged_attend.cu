@@ -418,19 +418,22 @@ __device__ __forceinline__ int2 share_start(const int32_t* before, int n_tiles, 
 }
 
 // ---------------------------------------------------------------------------
-// schedule: the list of a call with many tiles, one CTA.
+// schedule: the list of a call where the attention's CTAs do not make it, one
+// CTA; as many threads as a short list has tiles (4.7 us for 128 tiles of 16
+// requests; 1,024 threads 6.5).
 // ---------------------------------------------------------------------------
 constexpr int kSchedThreads = 1024;
 
-__global__ void __launch_bounds__(kSchedThreads) schedule_paged_kernel(PagedAttendArgs a, int N) {
+template <int kThreads, int kTiles, int kRequests>
+__global__ void __launch_bounds__(kThreads) schedule_paged_kernel(PagedAttendArgs a, int N) {
   __shared__ List t;
-  __shared__ int32_t off[kMaxRequests + 1], before[kListTiles];
+  __shared__ int32_t off[kRequests + 1], before[kTiles];
   launch_dependents();
-  build_list<kSchedThreads, kListTiles>(a, N, off, before, t, true);
+  build_list<kThreads, kTiles>(a, N, off, before, t, true);
   __syncthreads();
-  for (int r = threadIdx.x; r <= a.R; r += kSchedThreads) a.tile_off[r] = off[r];
+  for (int r = threadIdx.x; r <= a.R; r += kThreads) a.tile_off[r] = off[r];
   if (t.used > 0)
-    for (int w = threadIdx.x; w <= t.used; w += kSchedThreads) a.start[w] = share_start(before, t.n_tiles, t.units, t.used, w);
+    for (int w = threadIdx.x; w <= t.used; w += kThreads) a.start[w] = share_start(before, t.n_tiles, t.units, t.used, w);
 }
 
 // The segments of one CTA, in order; every warp that walks them calls next()
@@ -1368,7 +1371,10 @@ cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
     attend_paged_kernel<N, kQ4><<<a.workers, C::kThreads, C::kSmem, s>>>(a, maps);
     e = cudaGetLastError();
   } else {
-    schedule_paged_kernel<<<1, kSchedThreads, 0, s>>>(a, N);
+    if (a.few_tiles)
+      schedule_paged_kernel<kOwnTiles, kOwnTiles, kOwnTiles><<<1, kOwnTiles, 0, s>>>(a, N);
+    else
+      schedule_paged_kernel<kSchedThreads, kListTiles, kMaxRequests><<<1, kSchedThreads, 0, s>>>(a, N);
     e = cudaGetLastError();
     if (e == cudaSuccess) e = launch_after(attend_paged_kernel<N, kQ4>, a.workers, C::kThreads, C::kSmem, s, a, maps);
   }
@@ -1412,7 +1418,8 @@ cudaError_t launch_paged_attend(const PagedAttendArgs& args, bool q4, cudaStream
   const int N = paged_tile_rows(a.R, a.n_tokens, a.H);
   // A list that is short whatever the requests' shares of the tokens are is built by each CTA: no launch before the
   // attention.  Measured, 16 heads: one request of 4k 15.4 us, with the kernel that lists 18.1; 64 of 1k 34.5 and 39.8.
-  a.own_list = !(q4 && N == 64) && a.R <= kOwnTiles && a.R + ((int64_t)a.n_tokens * a.H + N - 1) / N <= kOwnTiles;
+  a.few_tiles = a.R <= kOwnTiles && a.R + ((int64_t)a.n_tokens * a.H + N - 1) / N <= kOwnTiles;
+  a.own_list = !(q4 && N == 64) && a.few_tiles;
   if (q4) return N == 16 ? launch<16, true>(a, s) : N == 32 ? launch<32, true>(a, s) : launch<64, true>(a, s);
   return N == 16 ? launch<16, false>(a, s) : N == 32 ? launch<32, false>(a, s) : launch<64, false>(a, s);
 }
