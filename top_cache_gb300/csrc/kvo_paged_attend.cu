@@ -554,8 +554,8 @@ __device__ __forceinline__ int64_t pool_row(const PagedAttendArgs& a, const int3
   return b < 0 || (int64_t)b >= a.n_blocks ? -1 : (int64_t)b * a.B + (t - j * a.B);
 }
 
-// One block's codes and scales of producer thread (token, side): of each pair
-// the 64 elements of slab 2 i + side, of the rope slab 32 elements.
+// One block's codes and scales of producer thread (token, side): of each slab
+// 32 elements.
 struct Codes {
   uint4 c[4][2];
   uint32_t s[4];
@@ -699,7 +699,8 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       if (!landed) fail();
     } else {
       // ---- producers, 4 bits ------------------------------------------------------------
-      // thread (token, side): slab 2 i + side of pair i
+      // thread (token, side): half `side` of each of pair i's two slabs, so that two lanes read 32 bytes side by side;
+      // the scales of slab 2 i + side
       const int pt = tid - kSoftThreads, tok = pt >> 1, side = pt & 1;
       // 16-byte chunk c of this token's 128 bytes of a slab lies at (chunk0 + slab) ^ (c << 4)
       const uint32_t chunk0 = (uint32_t)tok * 128u + ((uint32_t)(tok & 7) << 4);
@@ -737,9 +738,9 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         k.c[i][0] = k.c[i][1] = make_uint4(0u, 0u, 0u, 0u);
         k.s[i] = 0u;
         if (crow) {
-          const uint4* p = reinterpret_cast<const uint4*>(crow + (2 * i + side) * 32);
+          const uint4* p = reinterpret_cast<const uint4*>(crow + i * 64 + side * 16);
           k.c[i][0] = __ldg(p);
-          k.c[i][1] = __ldg(p + 1);
+          k.c[i][1] = __ldg(p + 2);
           k.s[i] = __ldg(reinterpret_cast<const uint32_t*>(srow + (2 * i + side) * 4));
         }
       };
@@ -809,21 +810,19 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           for (int i = 0; i < 4; ++i) {
             const int x = 4 * g + i, slot = x % C::kRing, use = x / C::kRing;
             if (use >= 1 && !wait(&B.e_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
-            const uint32_t dst = sb + C::kRingOff + (uint32_t)slot * kPair + (uint32_t)side * kSlab + chunk0;
-            uint32_t sc[4];
-            scales2(k.s[i] & 0xffffu, sc[0], sc[1]);
-            scales2(k.s[i] >> 16, sc[2], sc[3]);
-            // a token's two threads start four chunks apart: the slabs share their banks
-            const uint32_t turn = (uint32_t)side << 6;
+            // eight lanes, both halves of four tokens' rows, write eight different chunks
+            const uint32_t dst = (sb + C::kRingOff + (uint32_t)slot * kPair + chunk0) ^ (uint32_t)side << 6;
+            const uint32_t other = __shfl_xor_sync(kFull, k.s[i], 1);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint4 c0 = k.c[i][q >> 1], c1 = k.c[i][(q >> 1) ^ 1];
-              const bool other = side;
-              const uint4 c = other ? c1 : c0;
-              uint4 lo, hi;
-              expand16(q & 1 ? c.z : c.x, q & 1 ? c.w : c.y, other ? sc[q ^ 2] : sc[q], lo, hi);
-              st_v4((dst ^ turn) ^ (uint32_t)(2 * q) << 4, lo);
-              st_v4((dst ^ turn) ^ (uint32_t)(2 * q + 1) << 4, hi);
+            for (int p = 0; p < 2; ++p) {
+              uint32_t s0, s1;
+              scales2(__byte_perm(side == p ? k.s[i] : other, 0u, side ? 0x4432 : 0x4410), s0, s1);
+              const uint4 c = k.c[i][p];
+              uint4 x[4];
+              expand16(c.x, c.y, s0, x[0], x[1]);
+              expand16(c.z, c.w, s1, x[2], x[3]);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) st_v4((dst + (uint32_t)p * kSlab) ^ (uint32_t)q << 4, x[q]);
             }
             mbar_arrive(&B.e_full[slot]);
             if (pre) load_pair(i);
