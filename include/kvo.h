@@ -540,7 +540,8 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
  *   status      : device uint32, nullable: set to 0, then nonzero if a bounded
  *                 wait expired (KVO_SELECT_ERR_TIMEOUT) or cu_tokens decreases
  *                 (KVO_SELECT_ERR_PLAN); the outputs are then not valid
- * Precision: scores and sums in fp32 on exact products; the softmax weights of
+ * Precision: scores and sums in fp32 on exact products (KVO_CACHE_Q4: a query
+ * element more than 2^31 below its row's largest loses bits); the softmax weights of
  * the value product are rounded to bf16 (KVO_CACHE_Q4: fp16), their sum is not;
  * out is rounded to bf16.  The same inputs give the same bits.
  * Errors (nothing launched): KVO_EINVAL, KVO_ECUDA.

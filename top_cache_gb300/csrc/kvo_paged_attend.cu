@@ -40,17 +40,19 @@
 // stop.
 //
 // What bounds it (152 CTAs, clocks of one block of 128 tokens at N = 64).  16
-// bits: S^T 1,750 + O^T 1,550 at the operands' shared-memory rate; the softmax
-// between them, 950, is exposed, since the ring has room for one block and no
-// more, and 400-700 go by until the first pair is refilled: 4,800 to 5,000, 0.39
+// bits: S^T 1,730 + O^T 1,520 at the operands' shared-memory rate; the softmax
+// between them, 1,550 with its hand-overs, is exposed, since the ring has room
+// for one block and no more: 4,800.  Borders of tiles cost 2,000 and more.  0.39
 // of the measured bf16 rate on 16 x 4 positions of 128 heads over a window of
-// 4,096 (99 us).  4 bits: the expansion writes another 147 KB a block through the
-// same 128 bytes a clock, 6,300.  N = 16 reads 16 bits at 5.4 to 5.5 TB/s (0.80
-// of the copy rate: 32 requests of 32k, 155 us), 4 bits at 2.1 TB/s, bound by the
-// expansion and the products' operand reads (5,300 clocks a block).
+// 4,096 (99 us).  4 bits: the expansion's stores add 1,150 clocks to the 3,300 of
+// operand reads, and take 1,000 a pair while O^T is read: 6,200.  N = 16 reads 16
+// bits at 5.4 to 5.5 TB/s (0.80 of the copy rate: 32 requests of 32k, 154 us).  4
+// bits: 2.2 TB/s, 5,250 clocks a block: 2,450 of operand reads beside 3,000
+// wavefronts of the load/store path (1,400 stores, 1,400 loads of codes).
 // Tried and slower: blocks of 64 tokens with S^T two blocks ahead (the M = 64
 // product does not repay twice the hand-overs), keys in TMEM for S^T of 4-bit
-// tiles (150 clocks a product), 16 softmax warps (their time is latency).
+// tiles (150 clocks a product), 16 softmax warps (their time is latency), 16
+// producer warps at N = 16 (231 us for 218), weights stored before the vote.
 //
 // Split.  The tiles are listed with their blocks.  If whole tiles would leave
 // CTAs idle (few tiles, or uneven ones), the list's blocks are cut evenly over
