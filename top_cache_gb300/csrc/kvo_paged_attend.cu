@@ -210,9 +210,9 @@ __device__ __forceinline__ bool phase_wait(uint64_t* bar, uint32_t parity, uint6
 __device__ __forceinline__ uint32_t swz(uint32_t slab, int r, int c) {
   return slab + (uint32_t)r * 128u + ((uint32_t)(c ^ (r & 7)) << 4);
 }
-// The same box into L2 alone.
-__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+// Bytes (a multiple of 16, 16-byte aligned) into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 // A box of a 2-D tensor map (x: element, y: row), completion counted in bytes on bar.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -666,11 +666,8 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         for (int b = s.b0; b < s.b1; ++b, ++g) {
           const int row = next;
           next = find(b + 1);
-          if (next >= 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tma_prefetch(&maps.pool, 128 * i + 64 * (lane & 1), next);
-            if (!(lane & 1)) tma_prefetch(&maps.pool, kVal, next);
-          }
+          if (next >= 0)  // half of the run's rows
+            prefetch_l2(a.pool + ((int64_t)next + (lane & 1) * (run / 2)) * kRowBytes16, (uint32_t)(run / 2) * kRowBytes16);
           const uint32_t got = __popc(__ballot_sync(kFull, row >= 0)) >> 1;  // runs
           const uint32_t off = (uint32_t)((lane >> 1) * run) * 128u;
 #pragma unroll
