@@ -24,9 +24,9 @@
 // One persistent CTA per SM, warp-specialised:
 //   producers    the tile's queries, then each block's rows into a ring of
 //                pairs of 128-byte-swizzled K-major slabs (128 tokens x 64
-//                elements); the same bytes are the K-major A of S^T and the
+//                elements, atoms of 8 tokens of the two in turn); the same bytes are the K-major A of S^T and the
 //                MN-major A of O^T.  16 bits: one warp, a lane per TMA box of
-//                64 elements x the rows of one cache block (runs of 8 to 128).
+//                two slabs x the rows of one cache block (runs of 8 to 128).
 //                4 bits: 8 warps hold the next block's codes in registers while
 //                they expand this one's to fp16 (exact; queries are scaled by a
 //                power of two per row to fit fp16, undone in the scores)
@@ -91,6 +91,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr uint32_t kSlab = kBlk * 128;       // bytes of one slab of a block
 constexpr uint32_t kPair = 2 * kSlab;
+constexpr uint32_t kAtom = 1024;             // 8 tokens x 64 elements; a pair's two slabs alternate atom by atom
 constexpr int kMaxRing = 5;
 constexpr float kNone = -3.0e38f;            // running maximum before any visible token
 
@@ -131,8 +132,9 @@ struct Shape {
 
 // ---- tcgen05 ------------------------------------------------------------------------------
 // Shared-memory matrix descriptor, 128-byte swizzle: start address and leading offset (in 16-byte units) in the low
-// word; the high word is the same for every operand here: rows (or tokens) in groups of 8, 1 KB apart.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+// word; the high word: rows (or tokens) in groups of 8, 1 KB apart, or 2 KB in the ring.
+constexpr uint32_t kDescHigh = (kAtom >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescHighRing = (2 * kAtom >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t sdesc(uint32_t addr, uint32_t lead) {
   return ((addr >> 4) & 0x3FFFu) | (((lead >> 4) & 0x3FFFu) << 16);
 }
@@ -143,12 +145,13 @@ constexpr uint32_t idesc(bool bf16, int M, int N, bool a_mn_major, bool b_mn_maj
 }
 // Issued by the lane whose `el` is set; the warp runs it uniformly.  The operands live in uniform registers, and moving
 // one there costs more than the MMA's issue: only the descriptors' low words vary.
+template <uint32_t kHighA>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t el) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %7};\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(el), "n"(kDescHigh)
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(el), "n"(kHighA), "n"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t el) {
@@ -206,6 +209,10 @@ __device__ __forceinline__ bool phase_wait(uint64_t* bar, uint32_t parity, uint6
   }
 }
 // ---- shared memory -------------------------------------------------------------------------
+// 16-byte chunk c (0..7) of token r in slab `side` of a pair.
+__device__ __forceinline__ uint32_t swz_pair(uint32_t pair, int side, int r, int c) {
+  return pair + (uint32_t)(r >> 3) * (2 * kAtom) + (uint32_t)side * kAtom + (uint32_t)(r & 7) * 128u + ((uint32_t)(c ^ (r & 7)) << 4);
+}
 // 16-byte chunk c (0..7) of row r in a 128-byte-swizzled slab (1 KB aligned).
 __device__ __forceinline__ uint32_t swz(uint32_t slab, int r, int c) {
   return slab + (uint32_t)r * 128u + ((uint32_t)(c ^ (r & 7)) << 4);
@@ -219,6 +226,13 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+// A box of the pool's rows in two slabs (`slab`, + 1), from row 8 `group` on: see Maps.
+__device__ __forceinline__ void tma_pair(uint32_t dst, const CUtensorMap* map, int slab, int group, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(slab), "r"(group), "r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void st_v4(uint32_t addr, uint4 v) {
@@ -565,10 +579,14 @@ struct Codes {
   uint32_t rs;
 };
 
-// 16 bits: the pool's rows in boxes of 64 elements x `run` rows (the largest
-// power of two, at most 128, that divides block_tokens), the queries' in 64 x N.
+// 16 bits: the pool in boxes of `run` rows (the largest power of two, at most
+// 128, that divides block_tokens).  Value elements are seen as [row / 8][slab]
+// [row % 8][64]; a box has two slabs, so it lands as a pair's atoms do whatever
+// the run is.  (Small boxes bound the copy unit: 32 requests of 32k in blocks of
+// 8 tokens 179 us, with a box per slab 245; in blocks of 64, 152 either way.)
+// Rope: 64 elements x run; queries: 64 x N.
 struct Maps {
-  CUtensorMap pool, q;
+  CUtensorMap pool, rope, q;
   int run;
 };
 
@@ -655,11 +673,11 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         if (lane < kSlabs) tma_box(sb + C::kQOff + (uint32_t)lane * C::kQSlab, &maps.q, 64 * lane, s.grow, &B.q_full);
         ++tc;
         const int32_t* table = a.table + (int64_t)s.r * a.M;
-        // lane l holds the pool row of a block's run l / 2 (-1: not read): of this block, and of the next one, which is
-        // already on its way into L2 (the ring has room for little more than one)
+        // lanes l and l + 16 hold the pool row of a block's run l (-1: not read): of this block, and of the next one,
+        // which is already on its way into L2 (the ring has room for little more than one)
         auto find = [&](int b) -> int {
-          const int t = s.block(b) * kBlk + (lane >> 1) * run;
-          if (b >= s.b1 || (lane >> 1) >= runs || t > s.pmax || (t + run - 1 < s.lo && t >= a.sinks)) return -1;
+          const int t = s.block(b) * kBlk + (lane & 15) * run;
+          if (b >= s.b1 || (lane & 15) >= runs || t > s.pmax || (t + run - 1 < s.lo && t >= a.sinks)) return -1;
           return (int)pool_row(a, table, t);
         };
         int next = find(s.b0);
@@ -667,9 +685,9 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           const int row = next;
           next = find(b + 1);
           if (next >= 0)  // half of the run's rows
-            prefetch_l2(a.pool + ((int64_t)next + (lane & 1) * (run / 2)) * kRowBytes16, (uint32_t)(run / 2) * kRowBytes16);
+            prefetch_l2(a.pool + ((int64_t)next + (lane >> 4) * (run / 2)) * kRowBytes16, (uint32_t)(run / 2) * kRowBytes16);
           const uint32_t got = __popc(__ballot_sync(kFull, row >= 0)) >> 1;  // runs
-          const uint32_t off = (uint32_t)((lane >> 1) * run) * 128u;
+          const uint32_t off = (uint32_t)((lane & 15) * run) * 128u;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int x = 4 * g + i, slot = x % C::kRing, use = x / C::kRing;
@@ -677,16 +695,15 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(&B.e_full[slot], got * 2u * (uint32_t)run * 128u);
             __syncwarp();
             pairs = x + 1;
-            if (row >= 0)
-              tma_box(sb + C::kRingOff + (uint32_t)slot * kPair + (uint32_t)(lane & 1) * kSlab + off, &maps.pool,
-                      128 * i + 64 * (lane & 1), row, &B.e_full[slot]);
+            if (row >= 0 && lane < 16)
+              tma_pair(sb + C::kRingOff + (uint32_t)slot * kPair + 2 * off, &maps.pool, 2 * i, row >> 3, &B.e_full[slot]);
           }
           if (!ok) break;
           if (g >= 1 && !wait(&B.r_free, (uint32_t)(g - 1))) { ok = false; break; }
           if (lane == 0) mbar_arrive_expect_tx(&B.r_full, got * (uint32_t)run * 128u);
           __syncwarp();
           ropes = g + 1;
-          if (row >= 0 && !(lane & 1)) tma_box(sb + C::kRopeOff + off, &maps.pool, kVal, row, &B.r_full);
+          if (row >= 0 && lane < 16) tma_box(sb + C::kRopeOff + off, &maps.rope, kVal, row, &B.r_full);
         }
       }
       if (!ok) fail();
@@ -701,8 +718,8 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
       // thread (token, side): half `side` of each of pair i's two slabs, so that two lanes read 32 bytes side by side;
       // the scales of slab 2 i + side
       const int pt = tid - kSoftThreads, tok = pt >> 1, side = pt & 1;
-      // 16-byte chunk c of this token's 128 bytes of a slab lies at (chunk0 + slab) ^ (c << 4)
-      const uint32_t chunk0 = (uint32_t)tok * 128u + ((uint32_t)(tok & 7) << 4);
+      // 16-byte chunk c of this token's 128 bytes lies at (chunk0 + pair or slab) ^ (c << 4)
+      const uint32_t rope0 = swz(0u, tok, 0), pair0 = swz_pair(0u, 0, tok, 0);
       Codes k{};
       // The block whose cache block is being looked up runs two blocks ahead of the one being expanded, that whose
       // codes are being read one.
@@ -810,7 +827,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
             const int x = 4 * g + i, slot = x % C::kRing, use = x / C::kRing;
             if (use >= 1 && !wait(&B.e_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
             // eight lanes, both halves of four tokens' rows, write eight different chunks
-            const uint32_t dst = (sb + C::kRingOff + (uint32_t)slot * kPair + chunk0) ^ (uint32_t)side << 6;
+            const uint32_t dst = (sb + C::kRingOff + (uint32_t)slot * kPair + pair0) ^ (uint32_t)side << 6;
             const uint32_t other = __shfl_xor_sync(kFull, k.s[i], 1);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -821,14 +838,14 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
               expand16(c.x, c.y, s0, x[0], x[1]);
               expand16(c.z, c.w, s1, x[2], x[3]);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) st_v4((dst + (uint32_t)p * kSlab) ^ (uint32_t)q << 4, x[q]);
+              for (int q = 0; q < 4; ++q) st_v4((dst + (uint32_t)p * kAtom) ^ (uint32_t)q << 4, x[q]);
             }
             mbar_arrive(&B.e_full[slot]);
             if (pre) load_pair(i);
           }
           if (!ok) break;
           if (g >= 1 && !wait(&B.r_free, (uint32_t)(g - 1))) { ok = false; break; }
-          const uint32_t dst = (sb + C::kRopeOff + chunk0) ^ (uint32_t)side << 6;
+          const uint32_t dst = (sb + C::kRopeOff + rope0) ^ (uint32_t)side << 6;
           uint32_t s0, s1;
           scales2(k.rs, s0, s1);
           uint4 lo, hi;
@@ -852,7 +869,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
     constexpr uint32_t kIdS = idesc(!kQ4, kBlk, N, false, false);
     constexpr uint32_t kIdO = idesc(!kQ4, kBlk, N, true, C::kSharedP);
     const uint32_t ring_k = sdesc(sb + C::kRingOff, 16);     // K-major slabs
-    const uint32_t ring_v = sdesc(sb + C::kRingOff, kSlab);  // MN-major: two slabs, 128 value elements
+    const uint32_t ring_v = sdesc(sb + C::kRingOff, kAtom);  // MN-major: two slabs, 128 value elements
     const uint32_t rope = sdesc(sb + C::kRopeOff, 16);
     const uint32_t qd = sdesc(sb + C::kQOff, 16);
     const uint32_t pd = sdesc(sb + C::kPOff, 16);
@@ -870,7 +887,8 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           tc_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ss(dS, ring_k + (((uint32_t)slot * kPair + (uint32_t)(kk >> 2) * kSlab) >> 4) + (uint32_t)((kk & 3) * 2),
+            mma_ss<kDescHighRing>(
+                   dS, ring_k + (((uint32_t)slot * kPair + (uint32_t)(kk >> 2) * kAtom) >> 4) + (uint32_t)((kk & 3) * 2),
                    qd + (((uint32_t)(2 * i + (kk >> 2)) * C::kQSlab) >> 4) + (uint32_t)((kk & 3) * 2), kIdS,
                    (i | kk) ? 1u : 0u, el);
         }
@@ -879,7 +897,7 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
         tc_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ss(dS, rope + (uint32_t)(kk * 2), qd + ((8u * C::kQSlab) >> 4) + (uint32_t)(kk * 2), kIdS, 1u, el);
+          mma_ss<kDescHigh>(dS, rope + (uint32_t)(kk * 2), qd + ((8u * C::kQSlab) >> 4) + (uint32_t)(kk * 2), kIdS, 1u, el);
         mma_commit(&B.s_full, el);
         if (!C::kSharedP) mma_commit(&B.r_free, el);
         if (b + 1 == s.b1) mma_commit(&B.q_free, el);
@@ -895,8 +913,8 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
             // P^T: N = 64 MN-major (16 tokens are 2 KB), else K-major (64 tokens a slab of N rows)
             const uint32_t p = C::kSharedP ? pd + ((uint32_t)kk * 2048u >> 4)
                                            : pd + (((uint32_t)(kk >> 2) * (N * 128u)) >> 4) + (uint32_t)((kk & 3) * 2);
-            mma_ss(tmem + (uint32_t)(i * N), ring_v + (((uint32_t)slot * kPair + (uint32_t)kk * 2048u) >> 4), p, kIdO,
-                   (b > s.b0 || kk > 0) ? 1u : 0u, el);
+            mma_ss<kDescHighRing>(tmem + (uint32_t)(i * N), ring_v + (((uint32_t)slot * kPair + (uint32_t)kk * 4 * kAtom) >> 4),
+                                  p, kIdO, (b > s.b0 || kk > 0) ? 1u : 0u, el);
           }
           mma_commit(&B.e_free[slot], el);
         }
@@ -1095,11 +1113,11 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
           uint32_t edge = __ballot_sync(kFull, !all && odd);
           const int i = 2 * hw + (lane >> 4), x4 = 4 * g + i;  // this half's two pairs: 32 chunks of 8 elements
           if (!phase_wait(&B.e_full[x4 % C::kRing], (uint32_t)(x4 / C::kRing) & 1u, a.wait_ns)) fail();  // (S^T has read it)
-          const uint32_t slab = sb + C::kRingOff + (uint32_t)(x4 % C::kRing) * kPair + (uint32_t)((lane >> 3) & 1) * kSlab;
+          const uint32_t pair = sb + C::kRingOff + (uint32_t)(x4 % C::kRing) * kPair;
           while (edge) {
             const int r = 32 * quad + __ffs(edge) - 1;
             edge &= edge - 1u;
-            const uint32_t at = swz(slab, r, lane & 7);
+            const uint32_t at = swz_pair(pair, (lane >> 3) & 1, r, lane & 7);
             const uint4 x = ld_v4(at);
             constexpr uint32_t kExp = kQ4 ? 0x7c00u : 0x7f80u;
             uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -1328,6 +1346,18 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The value elements of the pool's rows as [row / 8][slab][row % 8][64] (the slabs' stride is less than a row's).
+bool encode_pairs(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
+  const EncodeTiled fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {64, 8, (cuuint64_t)(kVal / 64), (cuuint64_t)(rows / 8)};
+  const cuuint64_t strides[3] = {(cuuint64_t)kRowBytes16, 128, 8 * (cuuint64_t)kRowBytes16};
+  const cuuint32_t box[4] = {64, 8, 2, (cuuint32_t)(box_rows / 8)}, step[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A launch whose set-up may overlap the last one's end (it calls grid_wait before it reads anything).
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
@@ -1361,7 +1391,8 @@ cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
   if (!kQ4) {
     maps.run = a.B & -a.B;
     if (maps.run > kBlk) maps.run = kBlk;
-    if (!encode_rows(&maps.pool, a.pool, a.n_blocks * a.B, maps.run) ||
+    if (!encode_pairs(&maps.pool, a.pool, a.n_blocks * a.B, maps.run) ||
+        !encode_rows(&maps.rope, a.pool, a.n_blocks * a.B, maps.run) ||
         !encode_rows(&maps.q, a.q, (int64_t)a.n_tokens * a.H, N))
       return cudaErrorInvalidValue;
   }
