@@ -544,6 +544,9 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
  * element more than 2^31 below its row's largest loses bits); the softmax weights of
  * the value product are rounded to bf16 (KVO_CACHE_Q4: fp16), their sum is not;
  * out is rounded to bf16.  The same inputs give the same bits.
+ * A cached element that is not finite reaches only positions that see its row:
+ * they get NaN, or, where the row's score is -infinity, may get what they would
+ * without the row.
  * Errors (nothing launched): KVO_EINVAL, KVO_ECUDA.
  */
 size_t kvo_paged_attend_workspace_size(int32_t n_requests, int32_t n_tokens, int32_t n_heads,
