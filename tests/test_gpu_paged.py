@@ -8,6 +8,11 @@ truncate are off by n 2^-23 of the sum of magnitudes: 576 for a score, which mov
 by as much (and the sum of the weights by as much again), and the seen tokens for the
 weighted values and for the sum; 2^x adds 2^-21.
 """
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -18,6 +23,7 @@ from top_cache_gb300 import kvo as K
 pytestmark = pytest.mark.gpu
 
 SCALE = 1.0 / np.sqrt(192.0)
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BF16, Q4 = K.KVO_CACHE_BF16, K.KVO_CACHE_Q4
 
 
@@ -606,3 +612,45 @@ def test_tokens_that_decrease_are_reported():
         K.kvo_paged_attend(c.pool, c.n_blocks, 8, BF16, table, n, _dev(cu), q, SCALE, out, status=status)
         torch.cuda.synchronize()
         assert status.item() == 2 and bool((out == 0x1234).all())
+
+
+_FIRST_PLAN = """
+import torch
+from top_cache_gb300 import kvo as K
+R = %d
+z = lambda n, t=torch.int32: torch.zeros(n, dtype=t, device="cuda")
+ring, ends, slots, status = torch.arange(R, dtype=torch.int32, device="cuda"), z(2, torch.int64), z(R), z(R) + 5
+ends[1] = R
+K.kvo_paged_plan(z(R), z(R) + 1, 8, z(R).view(R, 1), ring, ends, ends, z(R), z(R), z(R + 1), slots, status)
+torch.cuda.synchronize()
+assert not status.any() and torch.equal(slots, 8 * ring), slots
+"""
+
+
+@pytest.mark.parametrize("R", [2443, 2444, 2457])
+def test_plan_as_the_first_call_of_a_process(R):
+    # the shared memory that a plan needs is asked for whatever its size is and whatever was called before
+    subprocess.run([sys.executable, "-c", _FIRST_PLAN % R], cwd=ROOT, check=True, timeout=300)
+
+
+def test_plans_of_two_threads():
+    # both need more shared memory than a launch has by default, one of them more than the other
+    failed = []
+
+    def plans(R):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                z = lambda n, t=torch.int32: torch.zeros(n, dtype=t, device="cuda")  # noqa: E731
+                a = (z(R), z(R), 8, z(R).view(R, 1), z(R), z(2, torch.int64), z(2, torch.int64), z(R), z(R), z(R + 1), z(1), z(R))
+                for _ in range(300):
+                    K.kvo_paged_plan(*a)
+                torch.cuda.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=plans, args=(R,)) for R in (4096, 2600)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed

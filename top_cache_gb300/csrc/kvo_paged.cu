@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kvo_paged.cuh"
 
 namespace kvo {
@@ -41,6 +43,8 @@ __device__ __forceinline__ int dead_end(int L, int B, int window, int sb) {
 // ---------------------------------------------------------------------------
 constexpr int kPlanCtas = 8;
 constexpr int kPlanSlots = 1024;  // slots that one CTA writes alone (1,024: 6.0 us as with eight; 4,096: 8.7 and 6.1)
+
+constexpr size_t plan_smem(int R) { return (5 * (size_t)R + 2) * 4; }  // bytes of the prefix arrays
 
 __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs a) {
   extern __shared__ int32_t sm[];
@@ -297,10 +301,16 @@ int rows_call(PagedRowsArgs& a, const void* rows, const int32_t* slots, int64_t 
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s) {
-  const size_t smem = (5 * (size_t)a.R + 2) * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(plan_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // Asked for once, for the most requests: what a launch may have does not depend on the calls before it or beside it.
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready{0};  // devices where the kernel may have its shared memory
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(plan_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(kMaxRequests));
     if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
   }
   const unsigned ctas = a.n_slots > kPlanSlots ? kPlanCtas : 1;
   cudaLaunchAttribute at{};
@@ -310,7 +320,7 @@ cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(ctas);
   c.blockDim = dim3(kPlanThreads);
-  c.dynamicSmemBytes = smem;
+  c.dynamicSmemBytes = plan_smem(a.R);
   c.stream = s;
   c.attrs = &at;
   c.numAttrs = 1;
