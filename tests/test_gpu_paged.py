@@ -654,3 +654,16 @@ def test_plans_of_two_threads():
     for t in threads:
         t.join()
     assert not failed
+
+
+def test_plan_of_the_longest_slot_list():
+    # 2^31 - 1 slots, 8 GB of them: the entries behind the new tokens are -1 to the last
+    n = 2 ** 31 - 1
+    z = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    slots = torch.full((n,), 7, dtype=torch.int32, device="cuda")
+    ends = torch.tensor([0, 2], dtype=torch.int64, device="cuda")
+    status = z(5, 5)
+    K.kvo_paged_plan(z(0, 3), z(9, -1), 16, z(-1, 4).view(2, 1), z(3, 2, -1), ends, ends, z(0, 0), z(0, 0), z(0, 0, 0), slots, status)
+    torch.cuda.synchronize()
+    assert status.tolist() == [0, 0] and slots[:9].tolist() == list(range(48, 57)) and ends.tolist() == [1, 3]
+    assert all(bool((part == -1).all()) for part in slots[9:].split(1 << 28))

@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs 
   int32_t* rel = nb + R;         // [R + 1] released blocks before each request
   int32_t* old = rel + R + 1;    // [R] cached tokens; -1: refused
   int32_t* ends = old + R;       // [R] 1: the request ends
-  const int tid = threadIdx.x, cta = blockIdx.x, step = kPlanThreads * gridDim.x;
+  const int tid = threadIdx.x, cta = blockIdx.x;
+  const uint32_t flat = cta * kPlanThreads + tid, step = kPlanThreads * gridDim.x;  // unsigned: 2^31 entries and a step pass an int
   const int sb = (a.sinks + B - 1) / B;
   const int64_t head = a.ring_in[0], tail = a.ring_in[1];
   const int64_t F = a.ring_size;
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs 
   const int n_new = taken, n_rel = rel[R];
   const auto ring_at = [&](int64_t i) -> int64_t { return i < F ? i : i - F; };
   const int64_t head0 = head < 0 ? 0 : head % F, tail0 = tail < 0 ? 0 : tail % F;
-  for (int r = cta * kPlanThreads + tid; r < R; r += step) {
+  for (int r = (int)flat; r < R; r += (int)step) {
     const int len = old[r], grow = cu[r + 1] - cu[r];
     a.cu_new[r] = cu[r];
     if (len >= 0) {
@@ -134,12 +135,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs 
     a.ring_out[0] = head + n_new;
     a.ring_out[1] = tail + n_rel;
   }
-  for (int i = cta * kPlanThreads + tid; i < n_new; i += step) {
+  for (uint32_t k = flat; k < (uint32_t)n_new; k += step) {
+    const int i = (int)k;
     // the last request that starts at or before entry i (those of its place that need none come before it)
     const int r = segment_of(nb, R, i);
     a.table[(int64_t)r * a.M + (old[r] + B - 1) / B + (i - nb[r])] = a.ring[ring_at(head0 + i)];
   }
-  for (int i = cta * kPlanThreads + tid; i < a.n_slots; i += step) {
+  for (uint32_t k = flat; k < (uint32_t)a.n_slots; k += step) {
+    const int i = (int)k;
     int32_t slot = -1;
     if (i < cu[R]) {
       const int r = segment_of(cu, R, i);
@@ -155,13 +158,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs 
   }
   if (n_rel == 0) return;
   plan_barrier();  // tables complete, and every taken entry of the ring read
-  for (int i = cta * kPlanThreads + tid; i < n_rel; i += step) {
+  for (uint32_t k = flat; k < (uint32_t)n_rel; k += step) {
+    const int i = (int)k;
     const int r = segment_of(rel, R, i);
-    const int k = i - rel[r], len = old[r];
-    int j = dead_end(len, B, a.window, sb) + k;
+    const int nth = i - rel[r], len = old[r];
+    int j = dead_end(len, B, a.window, sb) + nth;
     if (ends[r]) {
       const int s = min(sb, (len + B - 1) / B);
-      j = k < s ? k : j - s;
+      j = nth < s ? nth : j - s;
     }
     a.ring[ring_at(tail0 + i)] = a.table[(int64_t)r * a.M + j];
   }
