@@ -667,3 +667,28 @@ def test_plan_of_the_longest_slot_list():
     torch.cuda.synchronize()
     assert status.tolist() == [0, 0] and slots[:9].tolist() == list(range(48, 57)) and ends.tolist() == [1, 3]
     assert all(bool((part == -1).all()) for part in slots[9:].split(1 << 28))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("H", [4, 64])
+def test_lengths_that_do_not_fit_are_reported(fmt, H):
+    # a length past the block table, tokens past the queries or before them: nothing is computed, and the status says so
+    c = Cache([40, 9, 17], 8, fmt, 33)
+    full = c.M * 8
+    n = 6
+    q = torch.zeros(n, H, 576, dtype=torch.int16, device="cuda")
+    for many in (1, 100):
+        table = _dev(np.tile(c.table, (many, 1)))
+        rest = 3 * (many - 1)
+        for kv, cu, want in (([40, 9, 17], [0, 2, 4, 6], 0), ([full, 9, 17], [0, 2, 4, 6], 0), ([0, -1, 17], [0, 2, 2, 6], 0),
+                             ([full + 1, 9, 17], [0, 2, 4, 6], 2), ([40, 9, 2 ** 31 - 1], [0, 2, 4, 6], 2),
+                             ([40, 2 * full, 17], [0, 2, 2, 6], 2), ([40, 9, 17], [0, 2, 4, 7], 2),
+                             ([40, 9, 17], [-1, 2, 4, 6], 2), ([40, 9, 17], [0, 9, 9, 9], 2)):
+            out = torch.full((n, H, 512), 0x1234, dtype=torch.int16, device="cuda")
+            status = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+            # (requests without tokens behind the three)
+            K.kvo_paged_attend(c.pool, c.n_blocks, 8, fmt, table, _dev(kv + [0] * rest), _dev(cu + [cu[-1]] * rest), q, SCALE, out,
+                               status=status)
+            torch.cuda.synchronize()
+            assert status.item() == want, (kv, cu)
+            assert bool((out == 0x1234).all()) == (want != 0)

@@ -336,7 +336,13 @@ struct List {
 // Tiles per request; if they are few, the units before each, and how many CTAs share them evenly (0: each tile goes to
 // one CTA whole).  kThreads threads call it; `off` holds R + 1, `before` kMost entries.  publish: what the attention and
 // the join read is written to the workspace.
-constexpr int64_t kNoList = (int64_t)1 << 32;  // counted for a request whose tokens end before they start
+constexpr int64_t kNoList = (int64_t)1 << 32;  // counted for a request whose tokens or length are not what they may be
+// Its tokens end before they start, or lie outside the queries, or its cache ends behind its block table: cut to what
+// fits, its positions would be others.
+__device__ __forceinline__ bool misplaced(const PagedAttendArgs& a, int r) {
+  const int c0 = a.cu[r], c1 = a.cu[r + 1], kv = a.kv_lens[r];
+  return c0 < 0 || c1 < c0 || c1 > a.n_tokens || (int64_t)kv > (int64_t)a.M * a.B;
+}
 template <int kThreads, int kMost>
 __device__ __forceinline__ void build_list(const PagedAttendArgs& a, int N, int32_t* off, int32_t* before, List& t,
                                            bool publish) {
@@ -346,7 +352,7 @@ __device__ __forceinline__ void build_list(const PagedAttendArgs& a, int N, int3
   for (int base = 0; base < a.R; base += kThreads) {
     const int r = base + tid;
     int64_t n = 0;
-    if (r < a.R) n = a.cu[r + 1] < a.cu[r] ? kNoList : (request_rows(a, r) + N - 1) / N;
+    if (r < a.R) n = misplaced(a, r) ? kNoList : (request_rows(a, r) + N - 1) / N;
     const int64_t at = total + block_exclusive_sum<kThreads>(n, t.warp_sums, &sum);
     if (r < a.R) off[r] = (int32_t)at;
     total += sum;
