@@ -536,7 +536,8 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
  *                 rows from cu_tokens[n_requests] on are left as they were
  *   workspace   : device scratch, 256-byte aligned, at least
  *                 kvo_paged_attend_workspace_size() bytes (of the current
- *                 device; 0 on a bad argument); no initialisation, not
+ *                 device; 0 on a bad argument), which serve every call with
+ *                 no more requests, tokens and heads; no initialisation, not
  *                 preserved; one per call in flight
  *   status      : device uint32, nullable: set to 0, then nonzero if a bounded
  *                 wait (2 s) expired (KVO_SELECT_ERR_TIMEOUT), or cu_tokens

@@ -692,3 +692,20 @@ def test_lengths_that_do_not_fit_are_reported(fmt, H):
             torch.cuda.synchronize()
             assert status.item() == want, (kv, cu)
             assert bool((out == 0x1234).all()) == (want != 0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_workspace_serves_smaller_calls(fmt):
+    # fewer requests, tokens or heads: taller tiles of fewer requests need no more than the size says
+    R, T, H = 40, 40, 16
+    size = K.kvo_paged_attend_workspace_size(R, T, H)
+    for r, t, h in ((1, 40, 16), (1, 1, 16), (40, 2, 16), (39, 40, 15), (7, 31, 3), (2, 5, 1), (40, 40, 16), (1, 0, 1)):
+        assert 0 < K.kvo_paged_attend_workspace_size(r, t, h) <= size
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for lens, new, h in (([3000], [40], 16), ([700, 20], [4, 1], 16), ([5000], [1], 16), ([90] * 40, [1] * 40, 16),
+                         ([60] * 39, [1] * 39, 15), ([2000], [1], 1)):
+        c = Cache(lens, 16, fmt, 31)
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        q = O.bf16_bits(np.random.default_rng(32).standard_normal((int(cu[-1]), h, 576)))
+        out, lse = _attend(c, q, cu, lens, SCALE, workspace=ws)
+        _check(c, q, cu, lens, SCALE, 0, 0, out, lse, tokens={0, 1, int(cu[-1]) - 1})

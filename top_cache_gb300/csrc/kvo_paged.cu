@@ -416,7 +416,7 @@ size_t kvo_paged_attend_workspace_size(int32_t n_requests, int32_t n_tokens, int
   if (n_requests < 1 || n_requests > kvo::paged::kMaxRequests || n_tokens < 0 || n_heads < 1 || n_heads > 8192) return 0;
   int n_sm = 0;
   if (cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
-  return kvo::paged_attend_workspace(n_requests, n_tokens, n_heads, n_sm < kvo::paged::kMaxWorkers ? n_sm : kvo::paged::kMaxWorkers);
+  return kvo::paged_attend_workspace_most(n_requests, n_tokens, n_heads, n_sm < kvo::paged::kMaxWorkers ? n_sm : kvo::paged::kMaxWorkers);
 }
 
 int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,

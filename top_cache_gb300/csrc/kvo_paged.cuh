@@ -124,7 +124,8 @@ cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s);
 cudaError_t launch_paged_write(const PagedRowsArgs& a, bool q4, cudaStream_t s);
 cudaError_t launch_paged_read(const PagedRowsArgs& a, bool q4, cudaStream_t s);
 int paged_tile_rows(int n_requests, int n_tokens, int H);
-size_t paged_attend_workspace(int n_requests, int n_tokens, int H, int workers);
+size_t paged_attend_workspace(int n_requests, int n_tokens, int H, int workers);       // of this call
+size_t paged_attend_workspace_most(int n_requests, int n_tokens, int H, int workers);  // of every call no larger
 void paged_attend_carve(PagedAttendArgs& a, uint8_t* workspace);
 cudaError_t launch_paged_attend(const PagedAttendArgs& a, bool q4, cudaStream_t s);
 

@@ -1426,10 +1426,18 @@ int paged_tile_rows(int n_requests, int n_tokens, int H) {
   const int64_t rows = ((int64_t)n_tokens + n_requests - 1) / n_requests * H;
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
-size_t paged_attend_workspace(int n_requests, int n_tokens, int H, int workers) {
-  const size_t N = (size_t)paged_tile_rows(n_requests, n_tokens, H), W = (size_t)workers;
+// With tiles of N rows.
+static size_t workspace_of(size_t N, int n_requests, int workers) {
+  const size_t W = (size_t)workers;
   return 256 + up256(((size_t)n_requests + 1) * 4) + up256(kListTiles * sizeof(int2)) + up256((W + 1) * sizeof(int2)) +
          up256(W * sizeof(int4)) + up256(W * 4 * N * 4) + W * 2 * N * kVal * 4;
+}
+size_t paged_attend_workspace(int n_requests, int n_tokens, int H, int workers) {
+  return workspace_of((size_t)paged_tile_rows(n_requests, n_tokens, H), n_requests, workers);
+}
+// The tiles are highest where one request has all tokens.
+size_t paged_attend_workspace_most(int n_requests, int n_tokens, int H, int workers) {
+  return workspace_of((size_t)paged_tile_rows(1, n_tokens, H), n_requests, workers);
 }
 void paged_attend_carve(PagedAttendArgs& a, uint8_t* w) {
   const size_t N = (size_t)paged_tile_rows(a.R, a.n_tokens, a.H), W = (size_t)a.workers;
