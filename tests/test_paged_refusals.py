@@ -82,3 +82,13 @@ def test_binding_refuses_host_tensors():
         assert e.value.code == K.KVO_EINVAL
     with pytest.raises(K.KvoError):
         K.kvo_paged_block_bytes(7, 16)
+
+
+@pytest.mark.parametrize("block", [8, 24, 40, 65528, 65536])
+@pytest.mark.parametrize("fmt", [K.KVO_CACHE_BF16, K.KVO_CACHE_Q4])
+def test_largest_pool(L, block, fmt):
+    # n_blocks * block_tokens below 2^31, to the last block (calls of no rows touch nothing)
+    most = (2 ** 31 - 1) // block
+    for n, want in ((1, K.KVO_OK), (most, K.KVO_OK), (most + 1, K.KVO_EINVAL), (2 ** 62, K.KVO_EINVAL)):
+        assert L.kvo_paged_write(A, A, 0, A, n, block, fmt, None) == want, n
+        assert L.kvo_paged_read(A, n, block, fmt, A, 0, A, None) == want, n

@@ -281,7 +281,7 @@ int check_cache(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_
   if (format != KVO_CACHE_BF16 && format != KVO_CACHE_Q4) return fail(KVO_EINVAL, "unknown cache format");
   if (block_tokens < 8 || block_tokens > 65536 || block_tokens % 8 != 0)
     return fail(KVO_EINVAL, "block_tokens must be a multiple of 8 in 8 .. 65536");
-  if (n_blocks < 1 || n_blocks > ((int64_t)1 << 31) / block_tokens - 1)
+  if (n_blocks < 1 || n_blocks > INT32_MAX / block_tokens)
     return fail(KVO_EINVAL, "n_blocks * block_tokens must be positive and below 2^31");
   return KVO_OK;
 }
