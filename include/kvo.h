@@ -531,6 +531,7 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
  *                 (at most max_blocks * block_tokens; below 0: none)
  *   cu_tokens   : device int32 [n_requests + 1], not decreasing, from 0 up to n_tokens
  *   queries     : device bf16 [n_tokens][n_heads][576], 16-byte aligned; any n_heads <= 8192
+ *   scale       : finite, times log2 e too
  *   out         : device bf16 [n_tokens][n_heads][512] (written), 16-byte aligned
  *   lse         : device float [n_tokens][n_heads] (written), nullable
  *                 rows from cu_tokens[n_requests] on are left as they were

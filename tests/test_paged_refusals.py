@@ -92,3 +92,10 @@ def test_largest_pool(L, block, fmt):
     for n, want in ((1, K.KVO_OK), (most, K.KVO_OK), (most + 1, K.KVO_EINVAL), (2 ** 62, K.KVO_EINVAL)):
         assert L.kvo_paged_write(A, A, 0, A, n, block, fmt, None) == want, n
         assert L.kvo_paged_read(A, n, block, fmt, A, 0, A, None) == want, n
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3e38, -2.4e38, -float("inf")])
+def test_scales_that_are_not_finite_in_log2_units(L, scale):
+    # the kernel works in units of log2 e: 2.36e38 is the largest scale that stays finite there
+    a = {**ATTEND, "scale": ctypes.c_float(scale)}
+    assert L.kvo_paged_attend(*a.values()) == K.KVO_EINVAL and b"scale" in L.kvo_last_error()

@@ -439,7 +439,8 @@ int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, i
   if (!aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(cu_tokens, 4) || !aligned(lse, 4) || !aligned(status, 4))
     return fail(KVO_EINVAL, "array not aligned to its elements");
   if (!aligned(workspace, 256)) return fail(KVO_EINVAL, "workspace not 256-byte aligned");
-  if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return fail(KVO_EINVAL, "scale is not finite");
+  const float scale_log2 = scale * 1.4426950408889634f;  // log2 e
+  if (!(scale_log2 - scale_log2 == 0.f)) return fail(KVO_EINVAL, "scale, or scale * log2 e, is not finite");
   if (window < 0 || sinks < 0) return fail(KVO_EINVAL, "window and sinks must not be negative");
   int dev = 0, n_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -462,7 +463,7 @@ int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, i
   a.H = n_heads;
   a.window = (int32_t)(window < paged::kMaxTokens ? window : paged::kMaxTokens);
   a.sinks = (int32_t)(sinks < paged::kMaxTokens ? sinks : paged::kMaxTokens);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = status;
