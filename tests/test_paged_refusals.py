@@ -99,3 +99,24 @@ def test_scales_that_are_not_finite_in_log2_units(L, scale):
     # the kernel works in units of log2 e: 2.36e38 is the largest scale that stays finite there
     a = {**ATTEND, "scale": ctypes.c_float(scale)}
     assert L.kvo_paged_attend(*a.values()) == K.KVO_EINVAL and b"scale" in L.kvo_last_error()
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    # ctypes would pass their low bits: a window of 2^32 + 5 tokens as one of 5
+    i, x = torch.zeros(4, dtype=torch.int32), torch.zeros(4, 576, dtype=torch.bfloat16)
+    two, five = torch.zeros(2, dtype=torch.int64), torch.zeros(5, dtype=torch.int32)
+    pool = torch.zeros(4, 324 * 16, dtype=torch.uint8)
+    q, o = torch.zeros(4, 2, 576, dtype=torch.bfloat16), torch.zeros(4, 2, 512, dtype=torch.bfloat16)
+    plan = lambda block=16, **k: K.kvo_paged_plan(i, i, block, i.view(4, 1), i, two, two, i, i, five, i, i, **k)  # noqa: E731
+    attend = lambda n=4, **k: K.kvo_paged_attend(pool, n, 16, K.KVO_CACHE_Q4, i.view(4, 1), i, five, q, 0.1, o, **k)  # noqa: E731
+    calls = [("block_tokens", lambda n: plan(n)), ("window", lambda n: plan(window=n)), ("sinks", lambda n: plan(sinks=n)),
+             ("window", lambda n: attend(window=n)), ("sinks", lambda n: attend(sinks=n)), ("n_blocks", lambda n: attend(n)),
+             ("n_blocks", lambda n: K.kvo_paged_write(x, i, pool, n, 16, K.KVO_CACHE_Q4)),
+             ("n_blocks", lambda n: K.kvo_paged_read(pool, n, 16, K.KVO_CACHE_Q4, i, x)),
+             ("n_tokens", lambda n: K.kvo_paged_attend_workspace_size(1, n, 16)),
+             ("n_heads", lambda n: K.kvo_paged_attend_workspace_size(1, 1, n))]
+    for name, call in calls:
+        for n in (2 ** 31, 2 ** 32 + 5, 2 ** 64 + 4, -2 ** 31 - 1, -2 ** 64 + 4):
+            with pytest.raises(K.KvoError) as e:
+                call(n)
+            assert e.value.code == K.KVO_EINVAL and name in str(e.value)

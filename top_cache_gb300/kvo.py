@@ -378,6 +378,13 @@ def _sizes(t, name, dims):
     return t.shape, t.get_device()
 
 
+def _fits(**sizes):
+    """Sizes that the C ABI takes in 32 bits; ctypes would cut them to their low bits."""
+    for name, n in sizes.items():
+        if not -1 << 31 <= n < 1 << 31:
+            raise KvoError(KVO_EINVAL, "%s is out of range" % name)
+
+
 def _launch(f, args, device, stream):
     """f(*args, stream handle) with `device` current (the launches go there)."""
     T = _torch._C
@@ -396,6 +403,7 @@ def _launch(f, args, device, stream):
 
 def _pool(pool, n_blocks, block_tokens, format):
     """Address and device of a cache's pool, whose bytes must hold n_blocks blocks."""
+    _fits(n_blocks=n_blocks)
     if not isinstance(pool, _torch.Tensor) or not pool.is_cuda:
         raise KvoError(KVO_EINVAL, "pool must be a CUDA tensor")
     size = kvo_paged_block_bytes(format, block_tokens)
@@ -422,9 +430,11 @@ def kvo_paged_plan(lengths, new_tokens, block_tokens, block_table, ring, ring_in
     """
     t = _torch or _with_torch()
     i32, i64 = t.int32, t.int64
+    _fits(block_tokens=block_tokens, window=window, sinks=sinks)
     one, d = _sizes(lengths, "lengths", 1)
     (rows, M), F, S = _sizes(block_table, "block_table", 2)[0], _sizes(ring, "ring", 1)[0], _sizes(slots, "slots", 1)[0]
     R = one[0]
+    _fits(max_blocks=M, ring_size=F[0], n_slots=S[0])
     _launch(lib().kvo_paged_plan, (
         _dev(lengths, "lengths", i32, d, one), _dev(new_tokens, "new_tokens", i32, d, one), R, block_tokens, M, window,
         sinks, _dev(block_table, "block_table", i32, d, (R, M)), _dev(ring, "ring", i32, d, F), F[0],
@@ -459,6 +469,7 @@ def kvo_paged_attend_workspace_size(n_requests, n_tokens, n_heads, device=0):
     key = (n_requests, n_tokens, n_heads, device)
     n = _attend_sizes.get(key)
     if n is None:
+        _fits(n_requests=n_requests, n_tokens=n_tokens, n_heads=n_heads, device=device)
         n = int(lib().kvo_paged_attend_workspace_size(n_requests, n_tokens, n_heads, device))
         if len(_attend_sizes) >= 4096:
             _attend_sizes.clear()
@@ -478,8 +489,10 @@ def kvo_paged_attend(pool, n_blocks, block_tokens, format, block_table, kv_lens,
     """
     t = _torch or _with_torch()
     i32 = t.int32
+    _fits(window=window, sinks=sinks)
     p, d = _pool(pool, n_blocks, block_tokens, format)
     (T, H, _), (R, M) = _sizes(queries, "queries", 3)[0], _sizes(block_table, "block_table", 2)[0]
+    _fits(max_blocks=M)
     if workspace is None:
         size = kvo_paged_attend_workspace_size(R, T, H, d)
         if stream is None or _stream(stream) == t._C._cuda_getCurrentRawStream(d):
