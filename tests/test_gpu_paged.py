@@ -709,3 +709,34 @@ def test_a_workspace_serves_smaller_calls(fmt):
         q = O.bf16_bits(np.random.default_rng(32).standard_normal((int(cu[-1]), h, 576)))
         out, lse = _attend(c, q, cu, lens, SCALE, workspace=ws)
         _check(c, q, cu, lens, SCALE, 0, 0, out, lse, tokens={0, 1, int(cu[-1]) - 1})
+
+
+@pytest.mark.parametrize("block", [8, 40])
+def test_bytes_of_the_4_bit_cache(block):
+    """The written bytes are the definition's, and what the definition packs is read: neither call is the other's check."""
+    n_blocks, n = 3, 2 * block
+    bits = _special_rows(n, 34)
+    codes, scales = O.quantize(bits)
+    blocks = np.stack([O.pack_block(codes[i:i + block], scales[i:i + block]) for i in (0, block)])
+    order = np.array([2, 0])  # block of the first and of the second half of the rows
+    slots = (order[:, None] * block + np.arange(block)).reshape(-1)
+    pool = _pool(n_blocks, block, Q4)
+    K.kvo_paged_write(_dev(bits.view(np.int16), torch.int16), _dev(slots), pool, n_blocks, block, Q4)
+    torch.cuda.synchronize()
+    got = pool.cpu().numpy()
+    assert (got[1] == 0xA5).all()
+    nibbles = lambda b: np.stack([b & 15, b >> 4], -1)  # noqa: E731
+    a, b = nibbles(got[order, :288 * block]), nibbles(blocks[:, :288 * block])
+    assert np.array_equal(np.where(a == 8, 0, a), np.where(b == 8, 0, b))  # (a zero may have either sign)
+    assert np.array_equal(got[order, 288 * block:], blocks[:, 288 * block:])
+    # read back: bytes of every code and every scale, not only those that a write makes
+    g = np.random.default_rng(35)
+    codes, scales = g.integers(0, 16, (n, 576)).astype(np.uint8), g.integers(0, 128, (n, 36)).astype(np.uint8)
+    pool = torch.full_like(pool, 0xA5)
+    pool[torch.from_numpy(order).cuda()] = torch.from_numpy(
+        np.stack([O.pack_block(codes[i:i + block], scales[i:i + block]) for i in (0, block)])).cuda()
+    back = torch.full((n, 576), 0x1234, dtype=torch.int16, device="cuda")
+    K.kvo_paged_read(pool, n_blocks, block, Q4, _dev(slots), back)
+    torch.cuda.synchronize()
+    got = O.bf16_values(back.cpu().numpy().view(np.uint16))
+    assert np.array_equal(got, O.dequantize(codes, scales), equal_nan=True)
