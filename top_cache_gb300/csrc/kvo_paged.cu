@@ -38,11 +38,12 @@ __device__ __forceinline__ int dead_end(int L, int B, int window, int sb) {
 // inputs) the flat lists of new blocks, slots and released blocks are shared
 // out over all threads, each entry finding its request by a search in the
 // prefix arrays (shared memory).  A few KB to a few hundred KB are moved, so
-// latency is all it costs: 5.4 us for 16 requests, 9.2 for 509 requests with
-// 31,049 slots (34 with one CTA).
+// latency is all it costs (device time, L2 warm): 5.3 us for 16 requests, 11.4
+// for 509 requests of 61 new tokens at most, windowed, with 31,054 slots (13.3
+// with a cold L2; one CTA 37).
 // ---------------------------------------------------------------------------
 constexpr int kPlanCtas = 8;
-constexpr int kPlanSlots = 1024;  // slots that one CTA writes alone (1,024: 6.0 us as with eight; 4,096: 8.7 and 6.1)
+constexpr int kPlanSlots = 1024;  // slots that one CTA writes alone (1,029: 5.7 us, with eight 5.6; 4,101: 7.6 and 5.4)
 
 constexpr size_t plan_smem(int R) { return (5 * (size_t)R + 2) * 4; }  // bytes of the prefix arrays
 
@@ -173,8 +174,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_paged_kernel(PagedPlanArgs 
 
 // ---------------------------------------------------------------------------
 // Rows.  A thread handles one group of 16 elements (32 bytes of a bf16 row);
-// a CTA eight rows.  HBM bound: 65,531 rows into 4 bits 20.4 us (4.7 TB/s), out
-// of them 17.4 us (5.5 TB/s).
+// a CTA eight rows.  HBM bound, cold L2: 65,531 rows into the cache as bf16 25.4
+// us and out 25.5 (5.9 TB/s), into 4 bits 21.1 (4.6), out 17.1 (5.7).  A row goes
+// into 4 bits as 288 bytes of codes and 36 of scales in two places, 8 bytes and one
+// a thread, so its last sectors are written in part.  Not faster (20.5 and 17.4
+// then): 32-byte loads and stores (22.8 and 19.2 us), 4, 7 or 16 rows a CTA (22.9
+// to 25.1), no streaming hints (21.9 and 18.2).
 // ---------------------------------------------------------------------------
 constexpr int kRowsPerCta = 8;
 constexpr int kRowThreads = kRowsPerCta * kGroups;

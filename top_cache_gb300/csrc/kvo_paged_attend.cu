@@ -54,14 +54,23 @@
 // tiles (150 clocks a product), 16 softmax warps (their time is latency), 16
 // producer warps at N = 16 (231 us for 218), weights stored before the vote.
 //
-// Split.  The tiles are listed with their blocks.  If whole tiles would leave
-// CTAs idle (few tiles, or uneven ones), the list's blocks are cut evenly over
-// the CTAs, whatever tiles they cross, so one long request fills the GPU; a tile
-// that no CTA has alone leaves partial (O, m, l) in the workspace, at most two
-// per CTA, and a last kernel joins them in CTA order.  Else CTA c takes tiles c,
-// c + CTAs, ... whole (neighbours cost alike).  Measured, 16 heads: 128 requests
-// of 2k split 79 us, whole 62; 160 of 2k 97 and 105; 100 of 8k (4 bits) 145 and
-// 184.  Results do not depend on timing.
+// Split.  Up to 2,048 tiles are listed with their blocks.  If whole tiles would
+// leave CTAs idle (few tiles, or uneven ones), the list's blocks are cut evenly
+// over the CTAs, whatever tiles they cross, so one long request fills the GPU; a
+// tile that no CTA has alone leaves partial (O, m, l) in the workspace, at most
+// two per CTA, and a last kernel joins them in CTA order.  Else CTA c takes tiles
+// c, c + CTAs, ... whole (neighbours cost alike).  Measured, 16 heads: 128
+// requests of 2k split 68 us, whole 61; 160 of 2k 91 and 107; 100 of 8k (4 bits)
+// 135 and 182.  More than 2,048 tiles always go whole, however uneven they are:
+// 2,000 requests of 256 tokens and one of 256k 187 us, 2,100 and one 4,092 (apart
+// 137 and 70).  Results do not depend on timing.
+//
+// Rounding.  The weights of the value product are bf16 (fp16 over 4 bits), the
+// sum that divides it is of the weights before that, in fp32, so out may be off
+// by a weight's rounding where one token has nearly all of it.  A second sum, of
+// the rounded weights, kept in TMEM: error against 64 bits the same on normal
+// inputs (relative, root mean square, 0.0018 to 0.0021 with it and 0.0018 to
+// 0.0022 without), chunks of many tiles 2 to 5 % slower, others up to 4 %.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -81,11 +90,16 @@ namespace {
 
 constexpr int kBlk = 128;            // tokens per block of the walk: M of S^T, K of O^T
 constexpr int kSlabs = kRow / 64;    // 9: eight of the value, then rope
-constexpr int kListTiles = 2048;     // most tiles that are listed and split
+constexpr int kListTiles = 2048;     // most tiles that are listed, and may be split
 constexpr int kTileCost = 1;         // a tile's own cost, in blocks (queries in, output out)
-constexpr int kMinShare = 2;         // least units a CTA is given when the list is split
+// Least units a CTA is given when the list is split.  Measured with 1, 2, 4 (16 heads, us): one request of 1k 12.0, 14.0,
+// 16.3; of 4k 13.3, 15.0, 18.5; of 16k 18.2, 16.7, 19.7; of 64k 25.2 with each; 5 x 700 of 24 heads (4 bits) 23.0, 26.3,
+// 32.6; 32 of 32k 152 with each.  1 writes and joins more parts: faster up to 4k, slower at 16k.
+constexpr int kMinShare = 2;
 // What splitting over `used` of the CTAs costs, in blocks' time: one more launch that does something, and the parts
-// written and read (one or two of N x 2 KB a CTA).
+// written and read (one or two of N x 2 KB a CTA).  Measured as nothing, as this, as four times this (us): 128 requests
+// of 2k 68, 62, 62; 16 x 4 positions of 128 heads over a window of 4,096 108, 98, 97; a windowed chunk of 4,096 277, 279,
+// 278; 100 requests of 2k 56, 56, 51; 40 x 2 positions of 64 heads of 2k (4 bits) 59, 58, 72; one request of 1k 14, 14, 24.
 __device__ __forceinline__ int64_t split_cost(int N, int used, int workers) { return 2 + (int64_t)(N / 12) * used / workers; }
 constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
@@ -1224,9 +1238,11 @@ __global__ void __launch_bounds__(Shape<N, kQ4>::kThreads, 1)
 // every eighth part, and they meet in shared memory.  Latency bound: the list,
 // the parts' (m, l) and the parts themselves are read one after another, and the
 // kernel's code is cold.  So the loop over the parts stays short: 8,192 rows in 280
-// parts of 64, 36 MB, 5.8 us (two parts a turn 7.8, four 7.4); 512 rows 4.8 us (6.7,
+// parts of 64, 36 MB, 5.6 us (two parts a turn 7.8, four 7.4); 512 rows 4.8 us (6.7,
 // 7.3).  A CTA of 512 threads per four rows, with the weights in shared memory,
-// took 11.5 and 8.4 us; an empty list takes 2.0.
+// took 11.5 and 8.4 us; an empty list takes 1.8.  Teams where there are more warps
+// than rows: 16 rows of 64k tokens 9.0 us, a warp a row 40; 128 rows of 256k (4
+// bits) 8.5 and 31.9; 8,192 rows 5.6 and 5.4 (no team there).
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = kJoinWarps * 32;
@@ -1420,8 +1436,11 @@ cudaError_t launch(const PagedAttendArgs& a, cudaStream_t s) {
 }  // namespace
 
 // Rows per tile: the mean rows of a request, up to 64.  Measured, 16 requests of 32k, us with tiles of 16, 32, 64 rows:
-// 16 rows 112, 117, 124 (4 bits 93, 120, 136); 24 rows 207, 118, 125 (165, 121, 137); 48 rows 301, 215, 129 (237, 215,
-// 143); 128 rows 763, 407, 237 (598, 402, 251).
+// 16 rows 111, 115, 120 (4 bits 93, 119, 131); 24 rows 205, 116, 120 (161, 119, 132); 48 rows 297, 210, 123 (228, 210,
+// 136); 128 rows 756, 396, 223 (572, 390, 237).  One height for uneven requests is the best of the three, or within 2 %
+// of it, but short of two calls: 255 decode requests of 8k with a chunk of 512 tokens, 16 heads (mean 48 rows), 662, 529,
+// 524 (4 bits 866, 774, 640), apart 406 + 152 (322 + 205); 300 of 2k with a chunk of 200 (mean 32) 265, 201, 197, apart
+// 134 + 72.
 int paged_tile_rows(int n_requests, int n_tokens, int H) {
   const int64_t rows = ((int64_t)n_tokens + n_requests - 1) / n_requests * H;
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
@@ -1460,7 +1479,8 @@ cudaError_t launch_paged_attend(const PagedAttendArgs& args, bool q4, cudaStream
   PagedAttendArgs a = args;
   const int N = paged_tile_rows(a.R, a.n_tokens, a.H);
   // A list that is short whatever the requests' shares of the tokens are is built by each CTA: no launch before the
-  // attention.  Measured, 16 heads: one request of 4k 15.4 us, with the kernel that lists 18.1; 64 of 1k 34.5 and 39.8.
+  // attention.  Measured, 16 heads: one request of 4k 15.0 us, with the kernel that lists 17.7; 64 of 1k 22.0 and 24.0; at
+  // the limit, 128 of 1k 37.5 and 41.2, one chunk of 1,016 tokens 144.6 and 150.6.
   a.few_tiles = a.R <= kOwnTiles && a.R + ((int64_t)a.n_tokens * a.H + N - 1) / N <= kOwnTiles;
   a.own_list = !(q4 && N == 64) && a.few_tiles;
   if (q4) return N == 16 ? launch<16, true>(a, s) : N == 32 ? launch<32, true>(a, s) : launch<64, true>(a, s);
