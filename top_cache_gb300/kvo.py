@@ -486,6 +486,8 @@ def kvo_paged_attend(pool, n_blocks, block_tokens, format, block_table, kv_lens,
 
     workspace: uint8 CUDA tensor of kvo_paged_attend_workspace_size bytes; by default one is taken from the
     caching allocator on the stream of the call.
+    status: int32 CUDA tensor [1], set on the stream to 0 or to KVO_SELECT_ERR_* bits (lengths or tokens that do not
+    fit, a wait that expired: outputs not valid).  Nothing is read back here: without it such a call goes unnoticed.
     """
     t = _torch or _with_torch()
     i32 = t.int32
