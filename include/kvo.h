@@ -530,6 +530,7 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
  *   kv_lens     : device int32 [n_requests] cached tokens, the queries' own included
  *                 (at most max_blocks * block_tokens; below 0: none)
  *   cu_tokens   : device int32 [n_requests + 1], not decreasing, from 0 up to n_tokens
+ *                 (a plan's cu_new: past it where requests were refused)
  *   queries     : device bf16 [n_tokens][n_heads][576], 16-byte aligned; any n_heads <= 8192
  *   scale       : finite, times log2 e too
  *   out         : device bf16 [n_tokens][n_heads][512] (written), 16-byte aligned
@@ -542,9 +543,10 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
  *                 preserved; one per call in flight
  *   status      : device uint32, nullable: set to 0, then nonzero if a bounded
  *                 wait (2 s) expired (KVO_SELECT_ERR_TIMEOUT), or cu_tokens
- *                 decreases or leaves 0 .. n_tokens, or a kv_lens passes its
- *                 block table (KVO_SELECT_ERR_PLAN: nothing is computed); the
- *                 outputs are then not valid
+ *                 decreases, or leaves 0 .. n_tokens for a request whose
+ *                 kv_lens is not 0, or a kv_lens passes its block table
+ *                 (KVO_SELECT_ERR_PLAN: nothing is computed); the outputs are
+ *                 then not valid
  * Precision: scores and sums in fp32 on exact products (KVO_CACHE_Q4: a query
  * element more than 2^31 below its row's largest loses bits); the softmax weights of
  * the value product are rounded to bf16 (KVO_CACHE_Q4: fp16), their sum is not;

@@ -740,3 +740,24 @@ def test_bytes_of_the_4_bit_cache(block):
     torch.cuda.synchronize()
     got = O.bf16_values(back.cpu().numpy().view(np.uint16))
     assert np.array_equal(got, O.dequantize(codes, scales), equal_nan=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("H", [8, 64])
+def test_a_step_whose_tokens_pass_the_slots(fmt, H):
+    # the plan refuses the requests whose tokens pass the slots and counts their tokens all the same; the attention over
+    # as many query tokens computes the others, and gives nothing to those tokens of refused ones that it has
+    B, lens, new, T = 8, [30, 5, 20, 17], np.array([2, 9, 0, 3], np.int32), 4
+    c = Cache(lens, B, fmt, 36)
+    got = _run_plan(lens, new, B, c.table, np.array([-1], np.int32), np.array([0, 0]), T, 0, 0)  # (no block is needed)
+    assert got["status"].tolist() == [0, -3, 0, -3] and got["cu"].tolist() == [0, 2, 11, 11, 14]
+    last = int(c.table[0, 3]) * B
+    assert got["kv_lens"].tolist() == [32, 0, 20, 0] and got["slots"].tolist() == [last + 6, last + 7, -1, -1]
+    rows = O.bf16_bits(np.random.default_rng(37).standard_normal((T, 576)))
+    K.kvo_paged_write(_dev(rows.view(np.int16), torch.int16), _dev(got["slots"]), c.pool, c.n_blocks, B, fmt)
+    torch.cuda.synchronize()
+    c.refresh()
+    q = O.bf16_bits(np.random.default_rng(38).standard_normal((T, H, 576)))
+    out, lse = _attend(c, q, got["cu"], got["kv_lens"], SCALE)
+    _check(c, q, [0, 2], [32], SCALE, 0, 0, out, lse)
+    assert np.isneginf(lse[2:]).all() and not out[2:].any()

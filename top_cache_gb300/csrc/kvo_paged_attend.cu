@@ -351,11 +351,12 @@ struct List {
 // one CTA whole).  kThreads threads call it; `off` holds R + 1, `before` kMost entries.  publish: what the attention and
 // the join read is written to the workspace.
 constexpr int64_t kNoList = (int64_t)1 << 32;  // counted for a request whose tokens or length are not what they may be
-// Its tokens end before they start, or lie outside the queries, or its cache ends behind its block table: cut to what
-// fits, its positions would be others.
+// Its tokens end before they start, or its cache ends behind its block table, or tokens that see something lie outside
+// the queries: cut to what fits, its positions would be others.  (A plan counts the tokens of refused requests, which
+// may pass the queries; they see nothing.)
 __device__ __forceinline__ bool misplaced(const PagedAttendArgs& a, int r) {
   const int c0 = a.cu[r], c1 = a.cu[r + 1], kv = a.kv_lens[r];
-  return c0 < 0 || c1 < c0 || c1 > a.n_tokens || (int64_t)kv > (int64_t)a.M * a.B;
+  return c1 < c0 || (int64_t)kv > (int64_t)a.M * a.B || (kv > 0 && c1 > c0 && (c0 < 0 || c1 > a.n_tokens));
 }
 template <int kThreads, int kMost>
 __device__ __forceinline__ void build_list(const PagedAttendArgs& a, int N, int32_t* off, int32_t* before, List& t,
