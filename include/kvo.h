@@ -448,10 +448,15 @@ int kvo_attend(kvo_handle* h, const int32_t* units, int32_t n_units, const void*
  *                   elements; an element's value is its E2M1 code (element 2b
  *                   in the low four bits of byte b, 2b + 1 in the high ones)
  *                   times its group's E4M3 scale (324 bytes a row, not 1152)
+ *   KVO_CACHE_F8    a block is [block_tokens][576] E4M3 codes, then
+ *                   [block_tokens] fp32 scales, powers of two from 2^-32 to
+ *                   2^32 (any other reads as NaN); an element's value is its
+ *                   code times its row's scale (580 bytes a row)
  * kvo_paged_block_bytes: bytes of one block (0 on a bad argument).
  * ------------------------------------------------------------------------ */
 #define KVO_CACHE_BF16 0
 #define KVO_CACHE_Q4 1
+#define KVO_CACHE_F8 8
 int64_t kvo_paged_block_bytes(int32_t format, int32_t block_tokens);
 
 /*
@@ -507,9 +512,12 @@ int kvo_paged_plan(const int32_t* lengths, const int32_t* new_tokens, int32_t n_
  * group's scale is its largest magnitude / 6 rounded to E4M3 (nearest even, at
  * most 448), an element's code its quotient by that scale rounded to E2M1
  * (nearest, ties to the even code, at most 6); a group with an element that is
- * not finite reads back as NaN.
+ * not finite reads back as NaN.  KVO_CACHE_F8: the row's scale is the least
+ * power of two from 2^-32 to 2^32 with which no element passes 448, an
+ * element's code its quotient by that scale rounded to E4M3 (nearest even, at
+ * most 448); a row with an element that is not finite reads back as NaN.
  * kvo_paged_read: the values at slots[i] into row i of `rows` as bf16 (exact in
- * both formats); rows whose slot is skipped are left as they were.
+ * every format); rows whose slot is skipped are left as they were.
  * Errors: KVO_EINVAL, KVO_ECUDA.
  */
 int kvo_paged_write(const void* rows, const int32_t* slots, int64_t n_rows, void* pool,
@@ -548,8 +556,10 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
  *                 (KVO_SELECT_ERR_PLAN: nothing is computed); the outputs are
  *                 then not valid
  * Precision: scores and sums in fp32 on exact products (KVO_CACHE_Q4: a query
- * element more than 2^31 below its row's largest loses bits); the softmax weights of
- * the value product are rounded to bf16 (KVO_CACHE_Q4: fp16), their sum is not;
+ * element more than 2^31 below its row's largest loses bits; KVO_CACHE_F8: one more
+ * than 2^14 below); the softmax weights of the value product are rounded to bf16
+ * (KVO_CACHE_Q4: fp16; KVO_CACHE_F8: times their rows' scales, to as many bits as
+ * bf16 has in two terms, and to fewer below 2^-12 of the largest), their sum is not;
  * out is rounded to bf16.  The same inputs give the same bits.
  * A cached element that is not finite reaches only positions that see its row:
  * they get NaN, or, where the row's score is -infinity, may get what they would
@@ -564,6 +574,106 @@ int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, i
                      int32_t n_tokens, int32_t n_heads, float scale, int32_t window, int32_t sinks,
                      void* out, float* lse, void* workspace, size_t workspace_bytes,
                      uint32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Draft trees over the paged device cache (no passage of the pages; the
+ * library's own: drafted tokens that branch, where the positions of one step
+ * form a chain).  The query tokens of request r, cu_tokens[r] ..
+ * cu_tokens[r + 1] - 1, n of them, are the nodes of a tree: node 0 is its root
+ * (the token chosen last, whose row is not cached yet), and node i > 0 a draft
+ * below node parents[i] < i of the request.  Their rows are written to the
+ * request's last n places, so a step is
+ *   kvo_paged_plan (window 0, every request n_r >= 0), kvo_tree_masks;
+ *   for each layer kvo_paged_write, kvo_paged_attend_tree;
+ *   kvo_tree_accept, kvo_paged_commit, kvo_paged_move
+ * and may be captured into one graph.  A request that ends, does so in a plan
+ * of its own, with the window.  At most 1024 nodes a request.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kvo_tree_masks: node i's mask has bit j (bit j mod 32 of word j / 32) set
+ * when j is i or one of its ancestors.
+ *   parents   : device int32 [n_tokens]: within the request; a parent that is
+ *               negative, or not before its node, makes the node a root
+ *   cu_tokens : device int32 [n_requests + 1], as in kvo_paged_attend
+ *   masks     : device uint32 [n_tokens][mask_words] (written), mask_words 1 .. 32
+ *   depths    : device int32 [n_tokens] (written), nullable: a root's is 0
+ *   status    : device uint32, nullable: 0, or KVO_SELECT_ERR_PLAN if a request
+ *               has more than 32 * mask_words nodes (its masks and depths are 0)
+ * Rows of tokens that no request has are left as they were.
+ * Errors: KVO_EINVAL, KVO_ECUDA.
+ */
+int kvo_tree_masks(const int32_t* parents, const int32_t* cu_tokens, int32_t n_requests, int32_t n_tokens, uint32_t* masks,
+                   int32_t mask_words, int32_t* depths, uint32_t* status, void* stream);
+
+/*
+ * kvo_paged_attend_tree: kvo_paged_attend where node i of a request sees the
+ * request's context (its first kv_lens[r] - n tokens) and those nodes j <= i
+ * whose bit of i's mask is set.  With a window, node i is at position
+ * kv_lens[r] - n + depths[i], as query and as cached row, and sees what is
+ * less than `window` positions before it, or below `sinks`.  A request with
+ * kv_lens[r] < n sees nothing (0 and -inf).
+ *   masks, mask_words : as kvo_tree_masks writes them, or any others; a node
+ *                 without a bit there (j >= 32 * mask_words) is seen by none
+ *   depths      : device int32 [n_tokens], nullable when window is 0; taken as
+ *                 at least 0 and at most the node's index
+ * Everything else, and kvo_paged_attend_workspace_size, as for kvo_paged_attend.
+ */
+int kvo_paged_attend_tree(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,
+                          const int32_t* block_table, int32_t max_blocks, const int32_t* kv_lens, const int32_t* cu_tokens,
+                          int32_t n_requests, const uint32_t* masks, int32_t mask_words, const int32_t* depths,
+                          const void* queries, int32_t n_tokens, int32_t n_heads, float scale, int32_t window, int32_t sinks,
+                          void* out, float* lse, void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+
+/*
+ * kvo_tree_accept: the longest path from the root whose drafts are the tokens
+ * chosen at their parents (of paths as long, the one whose last node comes
+ * first).  The root is always on it.
+ *   drafted, chosen : device int32 [n_tokens]: every node's token; the token that
+ *               the model chose behind it
+ *   kv_lens   : device int32 [n_requests]; a request with fewer cached tokens
+ *               than nodes (a refused one), or more than 1024 nodes, or tokens
+ *               outside 0 .. n_tokens, accepts none
+ *   path      : device int32 [n_tokens] (written): behind cu_tokens[r], the
+ *               path's nodes from the root down, then -1
+ *   accepted  : device int32 [n_requests] (written): nodes on the path
+ *   next_tokens : device int32 [n_requests] (written), nullable: the token chosen
+ *               at the path's last node, -1 where none is accepted
+ * Errors: KVO_EINVAL, KVO_ECUDA.
+ */
+int kvo_tree_accept(const int32_t* parents, const int32_t* drafted, const int32_t* chosen, const int32_t* cu_tokens,
+                    const int32_t* kv_lens, int32_t n_requests, int32_t n_tokens, int32_t* path, int32_t* accepted,
+                    int32_t* next_tokens, void* stream);
+
+/*
+ * kvo_paged_commit: the requests' lengths after accepted[r] (0 .. n) of their n
+ * new tokens, and the blocks that then hold nothing put behind the end of the
+ * ring, in request and table order: those out of the window, which the plan with
+ * window 0 has left (as kvo_paged_plan gives them up), and those behind the
+ * new length.  Table entries stay.
+ *   lengths, kv_lens, cu_tokens, block_table, ring : of the step's plan
+ *   ring_in, ring_out : device int64 [2], may be the same
+ *   lengths_out : device int32 [n_requests], may be lengths: kv_lens[r] - n +
+ *                 accepted[r]; lengths[r] where n is 0 or kv_lens[r] < n
+ * Errors: KVO_EINVAL, KVO_ECUDA.
+ */
+int kvo_paged_commit(const int32_t* lengths, const int32_t* kv_lens, const int32_t* cu_tokens, const int32_t* accepted,
+                     int32_t n_requests, int32_t block_tokens, int32_t max_blocks, int32_t window, int32_t sinks,
+                     const int32_t* block_table, int32_t* ring, int32_t ring_size, const int64_t* ring_in,
+                     int64_t* ring_out, int32_t* lengths_out, void* stream);
+
+/*
+ * kvo_paged_move: the row of node path[k] to the place of node k, k = 0 ..
+ * accepted[r] - 1, in every one of n_pools pools (of n_blocks blocks each,
+ * pool_stride bytes apart, a multiple of 16): the accepted rows then stand
+ * behind the context in order.  The path's nodes ascend; a node that lies before
+ * its place, or is none of the request's, and rows of blocks that are not mapped
+ * are skipped.  kv_lens, cu_tokens and block_table as the attention had them.
+ * Errors: KVO_EINVAL, KVO_ECUDA.
+ */
+int kvo_paged_move(void* pools, int64_t pool_stride, int32_t n_pools, int64_t n_blocks, int32_t block_tokens, int32_t format,
+                   const int32_t* block_table, int32_t max_blocks, const int32_t* kv_lens, const int32_t* cu_tokens,
+                   int32_t n_requests, const int32_t* path, int32_t n_tokens, const int32_t* accepted, void* stream);
 
 /* ------------------------------------------------------------------------
  * Layerwise prefill offload ([LS] section 3 "Layerwise Prefill Offload":

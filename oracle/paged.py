@@ -1,6 +1,6 @@
 """Plain definitions of the paged device cache's operators, in Python and 64-bit numpy.
 
-Block plan (requests one after another), 4-bit rows (E2M1 codes, one E4M3 scale per 16
+Block plan (requests one after another), 8-bit rows, draft trees, 4-bit rows (E2M1 codes, one E4M3 scale per 16
 elements, both by exhaustive nearest value) and window attention (one query token at a
 time over the tokens that it sees).  Test infrastructure; shares nothing with the kernels.
 """
@@ -142,3 +142,142 @@ def attend(rows_of, q, positions, scale, window=0, sinks=0):
             dot[i] = abs(scale) * (np.abs(q[i]) @ np.abs(k).T).max(-1)
             lse[i] = (m + np.log(s))[:, 0]
     return out, lse, mag, dot, count
+
+
+# ---- 8-bit rows -------------------------------------------------------------------------------
+
+def quantize8(rows):
+    """bf16 bits [n][576] -> (codes [n][576], scale bits [n] uint32); a row that is not finite: 0, a NaN."""
+    x = bf16_values(rows)
+    fine = np.isfinite(x).all(-1)
+    x = np.where(fine[:, None], x, 0.0)
+    top = np.abs(x).max(-1)
+    exps = np.arange(-32, 33)
+    fits = top[:, None] <= 448.0 * 2.0 ** exps
+    e = np.where(fits.any(-1), exps[fits.argmax(-1)], 32)
+    a = np.abs(x) / (2.0 ** e)[:, None]
+    c = np.empty(a.shape, np.uint8)
+    for i in range(0, len(a), 256):
+        c[i:i + 256] = _nearest(a[i:i + 256], _E4M3)
+    c |= np.where(fine[:, None] & (bf16_bits_sign(rows) != 0), 128, 0).astype(np.uint8)
+    bits = (2.0 ** e).astype(np.float32).view(np.uint32)
+    return c, np.where(fine, bits, 0x7FC00000).astype(np.uint32)
+
+
+def bf16_bits_sign(bits):
+    return np.asarray(bits, np.uint16) >> 15
+
+
+def dequantize8(codes, scale_bits):
+    """float64 values [n][576]; a scale that is no power of two from 2^-32 to 2^32 reads as NaN."""
+    with np.errstate(invalid="ignore"):
+        s = np.asarray(scale_bits, np.uint32).view(np.float32).astype(np.float64)
+        m, e = np.frexp(np.where(np.isfinite(s), s, 0.0))
+    s = np.where((m == 0.5) & (e - 1 >= -32) & (e - 1 <= 32), s, np.nan)
+    grid = np.append(_E4M3, np.nan)
+    with np.errstate(invalid="ignore"):
+        return np.append(grid, -grid)[codes] * s[:, None]
+
+
+def pack_block8(codes, scale_bits):
+    """One block's bytes from its rows' codes and scales."""
+    return np.concatenate([codes.reshape(-1), np.ascontiguousarray(scale_bits, np.uint32).view(np.uint8)])
+
+
+# ---- draft trees ------------------------------------------------------------------------------
+
+def ancestors(parents):
+    """bool [n][n]: row i has i and its ancestors; a parent that is not before its node makes a root."""
+    n = len(parents)
+    a = np.zeros((n, n), bool)
+    for i, p in enumerate(parents):
+        if 0 <= p < i:
+            a[i] = a[p]
+        a[i, i] = True
+    return a
+
+
+def mask_words(a, words):
+    """int32 words [n][words] of boolean rows."""
+    b = np.zeros((len(a), 32 * words), np.uint8)
+    b[:, :a.shape[1]] = a
+    return np.packbits(b, axis=1, bitorder="little").view(np.int32).reshape(len(a), words)
+
+
+def accept(parents, drafted, chosen):
+    """The nodes of the longest path from node 0 whose drafts were chosen at their parents, the first of equals."""
+    best, paths = [], {}
+    for i, p in enumerate(parents):
+        if i == 0:
+            paths[0] = [0]
+        elif 0 <= p < i and p in paths and drafted[i] == chosen[p]:
+            paths[i] = paths[p] + [i]
+        if i in paths and len(paths[i]) > len(best):
+            best = paths[i]
+    return best
+
+
+def commit(lengths, kv_lens, new, accepted, block, table, ring, bounds, window=0, sinks=0):
+    """(lengths, ring, bounds) after `accepted` of the `new` tokens of every request."""
+    ring, out, back = ring.copy(), np.array(lengths, np.int32), []
+    keep = -(-sinks // block)
+
+    def hidden(L):
+        return set() if window == 0 else {j for j in range(keep, table.shape[1]) if (j + 1) * block - 1 < L - window + 1}
+
+    for r, n in enumerate(new):
+        if n <= 0 or kv_lens[r] < n or kv_lens[r] > table.shape[1] * block:
+            continue
+        first = kv_lens[r] - n
+        L = first + min(max(int(accepted[r]), 0), n)
+        out[r] = L
+        used = -(-L // block)
+        back += [int(table[r, j]) for j in range(used) if j in hidden(L) and j not in hidden(first)]
+        back += [int(table[r, j]) for j in range(used, -(-kv_lens[r] // block))]
+    for i, b in enumerate(back):
+        ring[(int(bounds[1]) + i) % len(ring)] = b
+    return out, ring, np.array([bounds[0], bounds[1] + len(back)], np.int64)
+
+
+def tree_seen(kv, n, masks, depths, t, window=0, sinks=0):
+    """bool [n][len(t)]: which of the tokens t (rows' places) node i sees; masks bool [n][n]."""
+    first = kv - n
+    t = np.asarray(t)
+    if first < 0:
+        return np.zeros((n, len(t)), bool)
+    depths = np.asarray(depths)
+    see = np.zeros((n, len(t)), bool)
+    for i in range(n):
+        j = t - first
+        own = j >= 0
+        inside = np.clip(j, 0, n - 1)
+        place = np.where(own, first + depths[inside], t)
+        see[i] = ~own | ((j < n) & (j <= i) & np.asarray(masks)[i, inside])
+        if window:
+            see[i] &= (place > first + depths[i] - window) | (place < sinks)
+    return see
+
+
+def attend_seen(rows, q, seen, scale):
+    """Attention of q [T][H][576] over rows [n][576], token i over those of seen[i].  Returns out, lse, and for the
+    tolerances sum_t w_t |v_t|, the largest |scale| sum_i |q_i k_ti|, the seen rows' number and the weights [T][H][n]."""
+    T, H = q.shape[:2]
+    out, lse = np.zeros((T, H, VAL)), np.full((T, H), -np.inf)
+    mag, dot, count = np.zeros((T, H, VAL)), np.zeros((T, H)), seen.sum(1)
+    weights = np.zeros((T, H, len(rows)))
+    for i in range(T):
+        at = np.flatnonzero(seen[i])
+        if len(at) == 0:
+            continue
+        k = rows[at]
+        with np.errstate(invalid="ignore", over="ignore"):
+            z = scale * (q[i] @ k.T)
+            m = z.max(-1, keepdims=True)
+            w = np.exp(z - m)
+            s = w.sum(-1, keepdims=True)
+            weights[i][:, at] = w / s
+            out[i] = (w / s) @ k[:, :VAL]
+            mag[i] = (w / s) @ np.abs(k[:, :VAL])
+            dot[i] = abs(scale) * (np.abs(q[i]) @ np.abs(k).T).max(-1)
+            lse[i] = (m + np.log(s))[:, 0]
+    return out, lse, mag, dot, count, weights

@@ -1,5 +1,5 @@
 // Paged device cache: block tables and slot maps built on the GPU, rows written
-// into the cache (16 bits, or quantized to 4) and read back.  Layout of a block:
+// into the cache (16 bits, or quantized to 8 or 4) and read back.  Layout of a block:
 // kvo_paged.cuh.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -268,32 +268,101 @@ __global__ void __launch_bounds__(kRowThreads) read_paged_kernel(PagedRowsArgs a
   __stcs(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
 }
 
+// 8 bits.  Eight lanes have a row, nine pieces of 8 elements each, so a row's
+// largest magnitude is three shuffles away and every piece is read once.
+constexpr int kRowLanes = 8;
+constexpr int kPieces = kRow / 8 / kRowLanes;
+constexpr int kRowThreadsF8 = 128;
+constexpr int kRowsPerCtaF8 = kRowThreadsF8 / kRowLanes;
+
+__global__ void __launch_bounds__(kRowThreadsF8) write_paged_f8_kernel(PagedRowsArgs a) {
+  const int l = threadIdx.x % kRowLanes;
+  const int64_t i = (int64_t)blockIdx.x * kRowsPerCtaF8 + threadIdx.x / kRowLanes;
+  const int32_t slot = i < a.n ? __ldg(a.slots + i) : -1;
+  const bool to = slot >= 0 && slot < a.pool_rows;
+  uint4 x[kPieces];
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    x[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (to) x[k] = __ldcs(reinterpret_cast<const uint4*>(a.rows + i * kRow) + l + k * kRowLanes);
+  }
+  // the largest magnitude, by its bits: NaN above infinity above every finite value
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    top = __vmaxu2(top, __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu));
+    top = __vmaxu2(top, __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
+  }
+#pragma unroll
+  for (int o = 1; o < kRowLanes; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, o));
+  if (!to) return;
+  top = max(top & 0xffffu, top >> 16);
+  // m 2^k <= 448 2^e = 1.75 2^(8 + e): the least e is k - 8 up to m = 1.75, else k - 7
+  const bool fine = top < 0x7f80u;
+  const int k0 = (int)(top >> 7) - 127;
+  const int e = min(max(k0 - 8 + ((top & 127u) > 96u ? 1 : 0), -kScaleExp), kScaleExp);
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+  const uint32_t blk = (uint32_t)slot / (uint32_t)a.B, in = (uint32_t)slot - blk * (uint32_t)a.B;
+  uint8_t* base = a.pool + (int64_t)blk * ((int64_t)a.B * kRowBytesF8);
+  uint2* dst = reinterpret_cast<uint2*>(base + (int64_t)in * kRow) + l;
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = __nv_cvt_float2_to_fp8x2(make_float2(bf_lo(w[j]) * down, bf_hi(w[j]) * down), __NV_SATFINITE, __NV_E4M3);
+    dst[k * kRowLanes] = fine ? make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16) : make_uint2(0u, 0u);
+  }
+  if (l == 0)
+    *reinterpret_cast<uint32_t*>(base + (int64_t)a.B * kRow + in * 4) = fine ? (uint32_t)(127 + e) << 23 : 0x7fffffffu;
+}
+
+__global__ void __launch_bounds__(kRowThreadsF8) read_paged_f8_kernel(PagedRowsArgs a) {
+  const int l = threadIdx.x % kRowLanes;
+  const int64_t i = (int64_t)blockIdx.x * kRowsPerCtaF8 + threadIdx.x / kRowLanes;
+  if (i >= a.n) return;
+  const int32_t slot = __ldg(a.slots + i);
+  if (slot < 0 || slot >= a.pool_rows) return;
+  const uint32_t blk = (uint32_t)slot / (uint32_t)a.B, in = (uint32_t)slot - blk * (uint32_t)a.B;
+  const uint8_t* base = a.pool + (int64_t)blk * ((int64_t)a.B * kRowBytesF8);
+  const uint2* src = reinterpret_cast<const uint2*>(base + (int64_t)in * kRow) + l;
+  uint2 c[kPieces];
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) c[k] = src[k * kRowLanes];
+  uint32_t bits = *reinterpret_cast<const uint32_t*>(base + (int64_t)a.B * kRow + in * 4);
+  if (!row_scale_valid(bits)) bits = 0x7fffffffu;
+  const float s = __uint_as_float(bits);
+  uint4* dst = reinterpret_cast<uint4*>(a.rows + i * kRow) + l;
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t two = (j < 2 ? c[k].x : c[k].y) >> (16 * (j & 1));
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
+      const float2 v = __half22float2(__half2(h));
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * s, v.y * s);  // exact
+      w[j] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    __stcs(dst + k * kRowLanes, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+
 template <typename K>
-cudaError_t launch_rows(K kernel, const PagedRowsArgs& a, cudaStream_t s) {
+cudaError_t launch_rows(K kernel, int rows_per_cta, int threads, const PagedRowsArgs& a, cudaStream_t s) {
   if (a.n <= 0) return cudaSuccess;
-  const int64_t grid = (a.n + kRowsPerCta - 1) / kRowsPerCta;
-  kernel<<<(unsigned)grid, kRowThreads, 0, s>>>(a);
+  const int64_t grid = (a.n + rows_per_cta - 1) / rows_per_cta;
+  kernel<<<(unsigned)grid, threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 int fail(int code, const char* msg) { return set_error(code, msg); }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// The cache's shape: KVO_OK, or the error that the calls below share.
-int check_cache(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format) {
-  if (!pool) return fail(KVO_EINVAL, "pool is NULL");
-  if (!aligned(pool, 16)) return fail(KVO_EINVAL, "pool not 16-byte aligned");
-  if (format != KVO_CACHE_BF16 && format != KVO_CACHE_Q4) return fail(KVO_EINVAL, "unknown cache format");
-  if (block_tokens < 8 || block_tokens > 65536 || block_tokens % 8 != 0)
-    return fail(KVO_EINVAL, "block_tokens must be a multiple of 8 in 8 .. 65536");
-  if (n_blocks < 1 || n_blocks > INT32_MAX / block_tokens)
-    return fail(KVO_EINVAL, "n_blocks * block_tokens must be positive and below 2^31");
-  return KVO_OK;
-}
-
 int rows_call(PagedRowsArgs& a, const void* rows, const int32_t* slots, int64_t n_rows, const void* pool,
               int64_t n_blocks, int32_t block_tokens, int32_t format) {
-  const int rc = check_cache(pool, n_blocks, block_tokens, format);
+  const int rc = check_paged_cache(pool, n_blocks, block_tokens, format);
   if (rc != KVO_OK) return rc;
   if (n_rows < 0 || n_rows >= (int64_t)1 << 31) return fail(KVO_EINVAL, "n_rows out of range");
   if (n_rows > 0 && (!rows || !slots)) return fail(KVO_EINVAL, "NULL argument");
@@ -308,6 +377,18 @@ int rows_call(PagedRowsArgs& a, const void* rows, const int32_t* slots, int64_t 
 }
 
 }  // namespace
+
+int check_paged_cache(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format) {
+  if (!pool) return fail(KVO_EINVAL, "pool is NULL");
+  if (!aligned(pool, 16)) return fail(KVO_EINVAL, "pool not 16-byte aligned");
+  if (format != KVO_CACHE_BF16 && format != KVO_CACHE_Q4 && format != KVO_CACHE_F8)
+    return fail(KVO_EINVAL, "unknown cache format");
+  if (block_tokens < 8 || block_tokens > 65536 || block_tokens % 8 != 0)
+    return fail(KVO_EINVAL, "block_tokens must be a multiple of 8 in 8 .. 65536");
+  if (n_blocks < 1 || n_blocks > INT32_MAX / block_tokens)
+    return fail(KVO_EINVAL, "n_blocks * block_tokens must be positive and below 2^31");
+  return KVO_OK;
+}
 
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s) {
   // Asked for once, for the most requests: what a launch may have does not depend on the calls before it or beside it.
@@ -335,11 +416,13 @@ cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s) {
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, plan_paged_kernel, a);
 }
-cudaError_t launch_paged_write(const PagedRowsArgs& a, bool q4, cudaStream_t s) {
-  return q4 ? launch_rows(write_paged_kernel<true>, a, s) : launch_rows(write_paged_kernel<false>, a, s);
+cudaError_t launch_paged_write(const PagedRowsArgs& a, int format, cudaStream_t s) {
+  if (format == KVO_CACHE_F8) return launch_rows(write_paged_f8_kernel, kRowsPerCtaF8, kRowThreadsF8, a, s);
+  return launch_rows(format == KVO_CACHE_Q4 ? write_paged_kernel<true> : write_paged_kernel<false>, kRowsPerCta, kRowThreads, a, s);
 }
-cudaError_t launch_paged_read(const PagedRowsArgs& a, bool q4, cudaStream_t s) {
-  return q4 ? launch_rows(read_paged_kernel<true>, a, s) : launch_rows(read_paged_kernel<false>, a, s);
+cudaError_t launch_paged_read(const PagedRowsArgs& a, int format, cudaStream_t s) {
+  if (format == KVO_CACHE_F8) return launch_rows(read_paged_f8_kernel, kRowsPerCtaF8, kRowThreadsF8, a, s);
+  return launch_rows(format == KVO_CACHE_Q4 ? read_paged_kernel<true> : read_paged_kernel<false>, kRowsPerCta, kRowThreads, a, s);
 }
 
 }  // namespace kvo
@@ -350,6 +433,7 @@ int64_t kvo_paged_block_bytes(int32_t format, int32_t block_tokens) {
   if (block_tokens < 8 || block_tokens > 65536 || block_tokens % 8 != 0) return 0;
   if (format == KVO_CACHE_BF16) return (int64_t)block_tokens * kvo::paged::kRowBytes16;
   if (format == KVO_CACHE_Q4) return (int64_t)block_tokens * kvo::paged::kRowBytesQ4;
+  if (format == KVO_CACHE_F8) return (int64_t)block_tokens * kvo::paged::kRowBytesF8;
   return 0;
 }
 
@@ -402,7 +486,7 @@ int kvo_paged_write(const void* rows, const int32_t* slots, int64_t n_rows, void
   kvo::PagedRowsArgs a{};
   const int rc = kvo::rows_call(a, rows, slots, n_rows, pool, n_blocks, block_tokens, format);
   if (rc != KVO_OK) return rc;
-  const cudaError_t e = kvo::launch_paged_write(a, format == KVO_CACHE_Q4, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = kvo::launch_paged_write(a, format, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return kvo::set_cuda_error(e, "paged write launch");
   return KVO_OK;
 }
@@ -412,7 +496,7 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
   kvo::PagedRowsArgs a{};
   const int rc = kvo::rows_call(a, rows, slots, n_rows, pool, n_blocks, block_tokens, format);
   if (rc != KVO_OK) return rc;
-  const cudaError_t e = kvo::launch_paged_read(a, format == KVO_CACHE_Q4, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = kvo::launch_paged_read(a, format, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return kvo::set_cuda_error(e, "paged read launch");
   return KVO_OK;
 }
@@ -424,13 +508,15 @@ size_t kvo_paged_attend_workspace_size(int32_t n_requests, int32_t n_tokens, int
   return kvo::paged_attend_workspace_most(n_requests, n_tokens, n_heads, n_sm < kvo::paged::kMaxWorkers ? n_sm : kvo::paged::kMaxWorkers);
 }
 
-int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,
-                     const int32_t* block_table, int32_t max_blocks, const int32_t* kv_lens, const int32_t* cu_tokens,
-                     int32_t n_requests, const void* queries, int32_t n_tokens, int32_t n_heads, float scale,
-                     int32_t window, int32_t sinks, void* out, float* lse, void* workspace, size_t workspace_bytes,
-                     uint32_t* status, void* stream) {
+// What kvo_paged_attend and kvo_paged_attend_tree share; masks null: causal order.
+static int paged_attend_call(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,
+                             const int32_t* block_table, int32_t max_blocks, const int32_t* kv_lens,
+                             const int32_t* cu_tokens, int32_t n_requests, const uint32_t* masks, int32_t mask_words,
+                             const int32_t* depths, const void* queries, int32_t n_tokens, int32_t n_heads, float scale,
+                             int32_t window, int32_t sinks, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, uint32_t* status, void* stream) {
   using namespace kvo;
-  const int rc = check_cache(pool, n_blocks, block_tokens, format);
+  const int rc = check_paged_cache(pool, n_blocks, block_tokens, format);
   if (rc != KVO_OK) return rc;
   if (!block_table || !kv_lens || !cu_tokens || !workspace) return fail(KVO_EINVAL, "NULL argument");
   if (n_requests < 1 || n_requests > paged::kMaxRequests) return fail(KVO_EINVAL, "n_requests must be in 1 .. 4096");
@@ -468,6 +554,9 @@ int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, i
   a.H = n_heads;
   a.window = (int32_t)(window < paged::kMaxTokens ? window : paged::kMaxTokens);
   a.sinks = (int32_t)(sinks < paged::kMaxTokens ? sinks : paged::kMaxTokens);
+  a.masks = masks;
+  a.mask_words = mask_words;
+  a.depths = depths;
   a.scale_log2 = scale_log2;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
@@ -476,9 +565,34 @@ int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, i
   a.workers = n_sm;
   a.device = dev;
   paged_attend_carve(a, static_cast<uint8_t*>(workspace));
-  const cudaError_t e = launch_paged_attend(a, format == KVO_CACHE_Q4, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_paged_attend(a, format, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_cuda_error(e, "paged attention launch");
   return KVO_OK;
+}
+
+int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,
+                     const int32_t* block_table, int32_t max_blocks, const int32_t* kv_lens, const int32_t* cu_tokens,
+                     int32_t n_requests, const void* queries, int32_t n_tokens, int32_t n_heads, float scale,
+                     int32_t window, int32_t sinks, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                     uint32_t* status, void* stream) {
+  return paged_attend_call(pool, n_blocks, block_tokens, format, block_table, max_blocks, kv_lens, cu_tokens, n_requests,
+                           nullptr, 0, nullptr, queries, n_tokens, n_heads, scale, window, sinks, out, lse, workspace,
+                           workspace_bytes, status, stream);
+}
+
+int kvo_paged_attend_tree(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format,
+                          const int32_t* block_table, int32_t max_blocks, const int32_t* kv_lens, const int32_t* cu_tokens,
+                          int32_t n_requests, const uint32_t* masks, int32_t mask_words, const int32_t* depths,
+                          const void* queries, int32_t n_tokens, int32_t n_heads, float scale, int32_t window, int32_t sinks,
+                          void* out, float* lse, void* workspace, size_t workspace_bytes, uint32_t* status, void* stream) {
+  using namespace kvo;
+  if (!masks && n_tokens != 0) return fail(KVO_EINVAL, "masks is NULL");
+  if (!aligned(masks, 4) || !aligned(depths, 4)) return fail(KVO_EINVAL, "array not aligned to its elements");
+  if (mask_words < 1 || mask_words > 32) return fail(KVO_EINVAL, "mask_words must be in 1 .. 32");
+  if (window > 0 && !depths && n_tokens != 0) return fail(KVO_EINVAL, "a window needs the nodes' depths");
+  return paged_attend_call(pool, n_blocks, block_tokens, format, block_table, max_blocks, kv_lens, cu_tokens, n_requests,
+                           masks, mask_words, depths, queries, n_tokens, n_heads, scale, window, sinks, out, lse, workspace,
+                           workspace_bytes, status, stream);
 }
 
 }  // extern "C"

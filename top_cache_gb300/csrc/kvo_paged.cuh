@@ -11,6 +11,10 @@
 //                   byte b, 2b + 1 in the high ones) times its group's E4M3
 //                   scale.  The product has at most 6 significant bits, so it
 //                   is exact in fp16 and in bf16.
+//   KVO_CACHE_F8    [block_tokens][576] E4M3 codes, then [block_tokens] fp32
+//                   scales, powers of two from 2^-32 to 2^32 (what is none of
+//                   them reads as NaN); an element's value is its code times
+//                   its row's scale: 4 significant bits, exact in bf16.
 #pragma once
 
 #include "kvo_internal.cuh"
@@ -25,6 +29,8 @@ constexpr int kGroups = kRow / kGroup;
 constexpr int kCodeBytes = kRow / 2;  // codes of one row
 constexpr int kRowBytesQ4 = kCodeBytes + kGroups;
 constexpr int kRowBytes16 = kRow * 2;
+constexpr int kRowBytesF8 = kRow + 4;
+constexpr int kScaleExp = 32;         // exponents of 8-bit rows' scales: -32 .. 32
 constexpr int kMaxRequests = 4096;    // per call: the requests' arrays fit shared memory
 constexpr int kMaxWorkers = 256;      // CTAs of the attention launch (one per SM)
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // tokens a block table reaches; rows of a pool are below 2^31
@@ -55,6 +61,11 @@ __device__ __forceinline__ int64_t block_exclusive_sum(int64_t v, int64_t* warp_
   __syncthreads();
   *total = warp_sums[kThreads / 32 - 1];
   return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+}
+
+// Whether bits are the scale of an 8-bit row: a power of two within the limits.
+__device__ __forceinline__ bool row_scale_valid(uint32_t bits) {
+  return (bits & 0x807fffffu) == 0u && (bits >> 23) - (127u - kScaleExp) <= 2u * kScaleExp;
 }
 
 // Largest i in [0, n) with off[i] <= x (off non-decreasing, off[0] <= x).
@@ -103,6 +114,9 @@ struct PagedAttendArgs {
   const uint16_t* q;       // [n_tokens][H][576]
   int32_t n_tokens, H;
   int32_t window, sinks;   // window 0: none
+  const uint32_t* masks;   // [n_tokens][mask_words], null: causal order
+  const int32_t* depths;   // [n_tokens] or null (no window)
+  int32_t mask_words;
   float scale_log2;
   uint16_t* out;           // [n_tokens][H][512]
   float* lse;              // [n_tokens][H] or null
@@ -121,12 +135,16 @@ struct PagedAttendArgs {
   float* part_o;           // [workers][2][N][512]
 };
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s);
-cudaError_t launch_paged_write(const PagedRowsArgs& a, bool q4, cudaStream_t s);
-cudaError_t launch_paged_read(const PagedRowsArgs& a, bool q4, cudaStream_t s);
+// The cache's shape: KVO_OK, or the error that every call on a pool gives.
+int check_paged_cache(const void* pool, int64_t n_blocks, int32_t block_tokens, int32_t format);
+cudaError_t launch_paged_write(const PagedRowsArgs& a, int format, cudaStream_t s);
+cudaError_t launch_paged_read(const PagedRowsArgs& a, int format, cudaStream_t s);
 int paged_tile_rows(int n_requests, int n_tokens, int H);
 size_t paged_attend_workspace(int n_requests, int n_tokens, int H, int workers);       // of this call
 size_t paged_attend_workspace_most(int n_requests, int n_tokens, int H, int workers);  // of every call no larger
 void paged_attend_carve(PagedAttendArgs& a, uint8_t* workspace);
-cudaError_t launch_paged_attend(const PagedAttendArgs& a, bool q4, cudaStream_t s);
+cudaError_t launch_paged_attend(const PagedAttendArgs& a, int format, cudaStream_t s);
+cudaError_t launch_paged_tree(const PagedAttendArgs& a, int N, bool q4, cudaStream_t s);  // kTree kernels
+cudaError_t launch_paged_f8(const PagedAttendArgs& a, int N, cudaStream_t s);             // 8 bits
 
 }  // namespace kvo

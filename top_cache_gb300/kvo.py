@@ -46,6 +46,7 @@ KVO_GATHER_LDG = 0
 KVO_GATHER_BULK = 1
 KVO_CACHE_BF16 = 0
 KVO_CACHE_Q4 = 1
+KVO_CACHE_F8 = 8
 
 EXPORTED = ("kvo_create", "kvo_destroy", "kvo_host_rows", "kvo_prefill", "kvo_append", "kvo_step",
             "kvo_select_workspace_size", "kvo_select", "kvo_reset", "kvo_profile_read",
@@ -53,7 +54,8 @@ EXPORTED = ("kvo_create", "kvo_destroy", "kvo_host_rows", "kvo_prefill", "kvo_ap
             "kvo_attend", "kvo_set_blocks", "kvo_host_block", "kvo_wait_selftest", "kvo_lw_create", "kvo_lw_destroy", "kvo_lw_plan", "kvo_lw_host_rows",
             "kvo_lw_set_length", "kvo_lw_begin", "kvo_lw_layer", "kvo_lw_layer_done", "kvo_lw_end",
             "kvo_lw_stats", "kvo_last_error", "kvo_paged_block_bytes", "kvo_paged_plan", "kvo_paged_write",
-            "kvo_paged_read", "kvo_paged_attend_workspace_size", "kvo_paged_attend")
+            "kvo_paged_read", "kvo_paged_attend_workspace_size", "kvo_paged_attend", "kvo_tree_masks",
+            "kvo_paged_attend_tree", "kvo_tree_accept", "kvo_paged_commit", "kvo_paged_move")
 
 
 class KvoConfig(ctypes.Structure):
@@ -178,6 +180,17 @@ def lib():
             L.kvo_paged_attend.restype = ctypes.c_int
             L.kvo_paged_attend.argtypes = [vp, i64, i32, i32, vp, i32, vp, vp, i32, vp, i32, i32,
                                            ctypes.c_float, i32, i32, vp, vp, vp, ctypes.c_size_t, vp, vp]
+            L.kvo_tree_masks.restype = ctypes.c_int
+            L.kvo_tree_masks.argtypes = [vp, vp, i32, i32, vp, i32, vp, vp, vp]
+            L.kvo_paged_attend_tree.restype = ctypes.c_int
+            L.kvo_paged_attend_tree.argtypes = [vp, i64, i32, i32, vp, i32, vp, vp, i32, vp, i32, vp, vp, i32, i32,
+                                                ctypes.c_float, i32, i32, vp, vp, vp, ctypes.c_size_t, vp, vp]
+            L.kvo_tree_accept.restype = ctypes.c_int
+            L.kvo_tree_accept.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp]
+            L.kvo_paged_commit.restype = ctypes.c_int
+            L.kvo_paged_commit.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp]
+            L.kvo_paged_move.restype = ctypes.c_int
+            L.kvo_paged_move.argtypes = [vp, i64, i32, i64, i32, i32, vp, i32, vp, vp, i32, vp, i32, vp, vp]
             _lib = L
     return _lib
 
@@ -414,10 +427,14 @@ def _pool(pool, n_blocks, block_tokens, format):
     return pool.data_ptr(), pool.get_device()
 
 
+_row_bytes = {KVO_CACHE_BF16: 1152, KVO_CACHE_Q4: 324, KVO_CACHE_F8: 580}
+
+
 def kvo_paged_block_bytes(format, block_tokens):
-    """Bytes of one block of a paged device cache (KVO_CACHE_BF16 or KVO_CACHE_Q4)."""
-    if format in (KVO_CACHE_BF16, KVO_CACHE_Q4) and 8 <= block_tokens <= 65536 and block_tokens % 8 == 0:
-        return block_tokens * (1152 if format == KVO_CACHE_BF16 else 324)
+    """Bytes of one block of a paged device cache (KVO_CACHE_BF16, KVO_CACHE_F8 or KVO_CACHE_Q4)."""
+    row = _row_bytes.get(format)
+    if row and 8 <= block_tokens <= 65536 and block_tokens % 8 == 0:
+        return block_tokens * row
     raise KvoError(KVO_EINVAL, "unknown cache format, or block_tokens not a multiple of 8 in 8 .. 65536")
 
 
@@ -478,6 +495,24 @@ def kvo_paged_attend_workspace_size(n_requests, n_tokens, n_heads, device=0):
     return n
 
 
+def _attend_workspace(workspace, pool, R, T, H, d, stream):
+    """The workspace of an attention call, by default from the caching allocator on the call's stream, and its size."""
+    t = _torch
+    if workspace is None:
+        size = kvo_paged_attend_workspace_size(R, T, H, d)
+        if stream is None or _stream(stream) == t._C._cuda_getCurrentRawStream(d):
+            workspace = t.empty(size, dtype=t.uint8, device=pool.device)
+        elif isinstance(stream, int):
+            # memory of the caching allocator belongs to the stream that it was taken on
+            raise KvoError(KVO_EINVAL, "a raw stream that is not the current one needs a workspace")
+        else:
+            with t.cuda.stream(stream):
+                workspace = t.empty(size, dtype=t.uint8, device=pool.device)
+    else:
+        size = _sizes(workspace, "workspace", 1)[0][0]
+    return workspace, size
+
+
 def kvo_paged_attend(pool, n_blocks, block_tokens, format, block_table, kv_lens, cu_tokens, queries, scale, out,
                      lse=None, window=0, sinks=0, workspace=None, status=None, stream=None):
     """Attention of queries (bf16 [T][H][576]) over the cache into out (bf16 [T][H][512]) and lse (float32 [T][H]
@@ -495,18 +530,7 @@ def kvo_paged_attend(pool, n_blocks, block_tokens, format, block_table, kv_lens,
     p, d = _pool(pool, n_blocks, block_tokens, format)
     (T, H, _), (R, M) = _sizes(queries, "queries", 3)[0], _sizes(block_table, "block_table", 2)[0]
     _fits(max_blocks=M)
-    if workspace is None:
-        size = kvo_paged_attend_workspace_size(R, T, H, d)
-        if stream is None or _stream(stream) == t._C._cuda_getCurrentRawStream(d):
-            workspace = t.empty(size, dtype=t.uint8, device=pool.device)
-        elif isinstance(stream, int):
-            # memory of the caching allocator belongs to the stream that it was taken on
-            raise KvoError(KVO_EINVAL, "a raw stream that is not the current one needs a workspace")
-        else:
-            with t.cuda.stream(stream):
-                workspace = t.empty(size, dtype=t.uint8, device=pool.device)
-    else:
-        size = _sizes(workspace, "workspace", 1)[0][0]
+    workspace, size = _attend_workspace(workspace, pool, R, T, H, d, stream)
     _launch(lib().kvo_paged_attend, (
         p, n_blocks, block_tokens, format, _dev(block_table, "block_table", i32, d, (R, M)), M,
         _dev(kv_lens, "kv_lens", i32, d, (R,)), _dev(cu_tokens, "cu_tokens", i32, d, (R + 1,)), R,
@@ -514,6 +538,98 @@ def kvo_paged_attend(pool, n_blocks, block_tokens, format, block_table, kv_lens,
         _dev(out, "out", _types16, d, (T, H, 512)), None if lse is None else _dev(lse, "lse", t.float32, d, (T, H)),
         _dev(workspace, "workspace", t.uint8, d, (size,)), size,
         None if status is None else _dev(status, "status", i32, d, (1,))), d, stream)
+
+
+def kvo_tree_masks(parents, cu_tokens, masks, depths=None, status=None, stream=None):
+    """Ancestor masks (int32 bits [T][words], written) and depths (int32 [T], written) of the requests' draft trees:
+    parents int32 [T] within a request, whose nodes are tokens cu_tokens[r] .. cu_tokens[r + 1] - 1 (int32 [R + 1])."""
+    t = _torch or _with_torch()
+    i32 = t.int32
+    (T, W), d = _sizes(masks, "masks", 2)
+    n = _sizes(cu_tokens, "cu_tokens", 1)[0][0]
+    _fits(n_tokens=T, mask_words=W)
+    _launch(lib().kvo_tree_masks, (
+        _dev(parents, "parents", i32, d, (T,)), _dev(cu_tokens, "cu_tokens", i32, d, (n,)), n - 1, T,
+        _dev(masks, "masks", i32, d, (T, W)), W, None if depths is None else _dev(depths, "depths", i32, d, (T,)),
+        None if status is None else _dev(status, "status", i32, d, (1,))), d, stream)
+
+
+def kvo_paged_attend_tree(pool, n_blocks, block_tokens, format, block_table, kv_lens, cu_tokens, masks, queries, scale,
+                          out, lse=None, depths=None, window=0, sinks=0, workspace=None, status=None, stream=None):
+    """kvo_paged_attend where a request's tokens are the nodes of a tree: each sees the context and the nodes of its mask
+    (int32 bits [T][words]); with a window, depths (int32 [T]) are their positions behind the context."""
+    t = _torch or _with_torch()
+    i32 = t.int32
+    _fits(window=window, sinks=sinks)
+    p, d = _pool(pool, n_blocks, block_tokens, format)
+    (T, H, _), (R, M) = _sizes(queries, "queries", 3)[0], _sizes(block_table, "block_table", 2)[0]
+    W = _sizes(masks, "masks", 2)[0][1]
+    _fits(max_blocks=M, mask_words=W)
+    workspace, size = _attend_workspace(workspace, pool, R, T, H, d, stream)
+    _launch(lib().kvo_paged_attend_tree, (
+        p, n_blocks, block_tokens, format, _dev(block_table, "block_table", i32, d, (R, M)), M,
+        _dev(kv_lens, "kv_lens", i32, d, (R,)), _dev(cu_tokens, "cu_tokens", i32, d, (R + 1,)), R,
+        _dev(masks, "masks", i32, d, (T, W)), W, None if depths is None else _dev(depths, "depths", i32, d, (T,)),
+        _dev(queries, "queries", _types16, d, (T, H, 576)), T, H, float(scale), window, sinks,
+        _dev(out, "out", _types16, d, (T, H, 512)), None if lse is None else _dev(lse, "lse", t.float32, d, (T, H)),
+        _dev(workspace, "workspace", t.uint8, d, (size,)), size,
+        None if status is None else _dev(status, "status", i32, d, (1,))), d, stream)
+
+
+def kvo_tree_accept(parents, drafted, chosen, cu_tokens, kv_lens, path, accepted, next_tokens=None, stream=None):
+    """The accepted path of every request's draft tree: its nodes into path (int32 [T]), their number into accepted, the
+    token chosen at its last node into next_tokens (int32 [R]); parents, drafted, chosen: int32 [T]."""
+    t = _torch or _with_torch()
+    i32 = t.int32
+    one, d = _sizes(parents, "parents", 1)
+    T, R = one[0], _sizes(kv_lens, "kv_lens", 1)[0][0]
+    _fits(n_tokens=T, n_requests=R)
+    _launch(lib().kvo_tree_accept, (
+        _dev(parents, "parents", i32, d, one), _dev(drafted, "drafted", i32, d, one), _dev(chosen, "chosen", i32, d, one),
+        _dev(cu_tokens, "cu_tokens", i32, d, (R + 1,)), _dev(kv_lens, "kv_lens", i32, d, (R,)), R, T,
+        _dev(path, "path", i32, d, one), _dev(accepted, "accepted", i32, d, (R,)),
+        None if next_tokens is None else _dev(next_tokens, "next_tokens", i32, d, (R,))), d, stream)
+
+
+def kvo_paged_commit(lengths, kv_lens, cu_tokens, accepted, block_tokens, block_table, ring, ring_in, ring_out,
+                     lengths_out, window=0, sinks=0, stream=None):
+    """Lengths (int32 [R]) after the accepted tokens of a draft step, and the blocks that then hold nothing back into the
+    ring (see kvo.h)."""
+    t = _torch or _with_torch()
+    i32, i64 = t.int32, t.int64
+    _fits(block_tokens=block_tokens, window=window, sinks=sinks)
+    one, d = _sizes(lengths, "lengths", 1)
+    M, F = _sizes(block_table, "block_table", 2)[0][1], _sizes(ring, "ring", 1)[0]
+    R = one[0]
+    _fits(max_blocks=M, ring_size=F[0], n_requests=R)
+    _launch(lib().kvo_paged_commit, (
+        _dev(lengths, "lengths", i32, d, one), _dev(kv_lens, "kv_lens", i32, d, one),
+        _dev(cu_tokens, "cu_tokens", i32, d, (R + 1,)), _dev(accepted, "accepted", i32, d, one), R, block_tokens, M, window,
+        sinks, _dev(block_table, "block_table", i32, d, (R, M)), _dev(ring, "ring", i32, d, F), F[0],
+        _dev(ring_in, "ring_in", i64, d, (2,)), _dev(ring_out, "ring_out", i64, d, (2,)),
+        _dev(lengths_out, "lengths_out", i32, d, one)), d, stream)
+
+
+def kvo_paged_move(pools, n_blocks, block_tokens, format, block_table, kv_lens, cu_tokens, path, accepted, n_pools=1,
+                   stream=None):
+    """The accepted paths' rows together behind their contexts, in each of n_pools pools of n_blocks blocks that lie in
+    `pools` one behind the other at equal distances."""
+    t = _torch or _with_torch()
+    i32 = t.int32
+    _fits(n_pools=n_pools)
+    if n_pools < 1:
+        raise KvoError(KVO_EINVAL, "n_pools must be positive")
+    size = kvo_paged_block_bytes(format, block_tokens)
+    p, d = _pool(pools, n_blocks, block_tokens, format)
+    stride, rest = divmod(pools.numel() * pools.element_size(), n_pools)
+    if rest or stride < n_blocks * size:
+        raise KvoError(KVO_EINVAL, "pools is not n_pools pools of n_blocks blocks")
+    (R, M), one = _sizes(block_table, "block_table", 2)[0], _sizes(path, "path", 1)[0]
+    _fits(max_blocks=M, n_tokens=one[0], n_requests=R)
+    _launch(lib().kvo_paged_move, (
+        p, stride, n_pools, n_blocks, block_tokens, format, _dev(block_table, "block_table", i32, d, (R, M)), M,
+        _dev(kv_lens, "kv_lens", i32, d, (R,)), _dev(cu_tokens, "cu_tokens", i32, d, (R + 1,)), R,
+        _dev(path, "path", i32, d, one), one[0], _dev(accepted, "accepted", i32, d, (R,))), d, stream)
 
 
 class Kvo:
