@@ -39,12 +39,11 @@ constexpr uint32_t kSlabF8 = kBlk * 128;       // 128 tokens x 128 elements
 constexpr uint32_t kPairF8 = 2 * kSlabF8;      // two slabs, in atoms of 8 tokens of each in turn
 constexpr uint32_t kRopeF8 = kBlk * 64;
 constexpr int kPairs = 2;                      // pairs of a block
-constexpr int kQWarps = 2, kQThreads = kQWarps * 32;
 constexpr int kMaxPairs = 5, kMaxRopes = 3;
 
 template <int N>
 struct ShapeF8 {
-  static constexpr int kThreads = kSoftThreads + kQThreads + 64;
+  static constexpr int kThreads = kSoftThreads + 64;
   static constexpr int kNC = N / 2;                        // rows of one softmax thread
   static constexpr int kRing = N == 64 ? 4 : kMaxPairs;    // pairs
   static constexpr int kRopes = N == 64 ? 1 : N == 32 ? 2 : kMaxRopes;
@@ -135,7 +134,7 @@ __device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, ui
 }
 
 struct BarsF8 {
-  uint64_t q_full, q_free, p_full, o_step, o_done, o_free, fin;
+  uint64_t q_full, p_full, o_step, o_done, o_free, fin;
   uint64_t s_full[2], r_full[kMaxRopes], r_free[kMaxRopes], e_full[kMaxPairs], e_free[kMaxPairs];
   uint32_t tmem, abort;
   uint32_t dead[2][2];  // softmax: a warp of the half gave up, by parity of the barrier's count
@@ -171,14 +170,13 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);
-  constexpr int kQ0 = kSoftWarps, kCopyWarp = kQ0 + kQWarps, kMmaWarp = kCopyWarp + 1;  // softmax warps first: whole lane quadrants
+  constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kCopyWarp + 1;  // softmax warps first: whole TMEM lane quadrants
   auto fail = [&]() {
     atomicOr(a.status, kErrTimeout);
     *abort_flag = 1u;
   };
   if (tid == 0) {
-    mbar_init(&B.q_full, kQThreads);
-    mbar_init(&B.q_free, 3);  // the last S^T done, and both softmax halves have seen the factors in place
+    mbar_init(&B.q_full, kSoftThreads);
     mbar_init(&B.p_full, kSoftThreads);
     mbar_init(&B.o_step, 1);
     mbar_init(&B.o_done, 1);
@@ -223,58 +221,7 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
   int tc = 0;  // segments with blocks so far
   const int64_t block_bytes = (int64_t)a.B * kRowBytesF8;
 
-  if (warp >= kQ0 && warp < kCopyWarp) {
-    // ---- queries: one warp per row; 2^-e brings the largest magnitude to at most 448 ---------
-    bool ok = true;
-    while (ok && walk.next(a, own, s)) {
-      if (s.b0 >= s.b1) continue;
-      if (tc >= 1 && !wait(&B.q_free, (uint32_t)(tc - 1))) { ok = false; break; }
-      for (int r = warp - kQ0; r < N; r += kQWarps) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(s.grow + r) * kRow);
-        uint4 v[3];
-        uint32_t top = 0u;
-#pragma unroll
-        for (int m = 0; m < 3; ++m) {
-          const int c = lane + 32 * m;
-          v[m] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < s.nrows && c < 72) v[m] = __ldg(src + c);
-          const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) top = max(top, max(w[x] & 0x7fffu, (w[x] >> 16) & 0x7fffu));
-        }
-        top = __reduce_max_sync(kFull, top);
-        const int e = min(max((int)(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0), -112), 120);
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int m = 0; m < 3; ++m) {
-          const int c = lane + 32 * m;
-          if (c < 72) {
-            const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float x0 = bf_lo(w[x]) * down, x1 = bf_hi(w[x]) * down;
-              hi[x] = e4m3_pair(x0, x1);
-              const float2 h = e4m3_values(hi[x]);
-              lo[x] = e4m3_pair((x0 - h.x) * 16.f, (x1 - h.y) * 16.f);
-            }
-            const uint32_t in = (uint32_t)(c & 1) * 8u;
-            const uint32_t to = c < 64 ? swz(sb + (uint32_t)(c >> 4) * C::kQSlab, r, (c & 15) >> 1)
-                                       : swz64(sb + C::kQRopeOff, r, (c - 64) >> 1);
-            st_v2(to + in, hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            // N rows further on the swizzle is the same
-            st_v2(to + in + (c < 64 ? N * 128u : N * 64u), lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-          }
-        }
-        // a query that is not finite has no finite score
-        if (lane == 0)
-          q_mul[(tc & 1) * N + r] = top < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fffffff);
-      }
-      mbar_arrive(&B.q_full);
-      ++tc;
-    }
-    if (!ok) fail();
-  } else if (warp == kCopyWarp) {
+  if (warp == kCopyWarp) {
     // ---- copies: lanes l and l + 16 hold the cache block and row of a block's run l (-1: not read): of this block, and of
     // the next one, which is already on its way into L2 ----------------------------------------
     const int run = maps.run, runs = kBlk / run;
@@ -291,6 +238,9 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
         const int32_t blk = __ldg(table + j);
         return blk < 0 || (int64_t)blk >= a.n_blocks ? -1 : blk;
       };
+      if (lane == 0 && tc > 0)  // the softmax warps read the tile's queries when the last tile's scores are done
+        prefetch_l2(a.q + (int64_t)s.grow * kRow, (uint32_t)s.nrows * (kRow * 2));
+      ++tc;
       int in_next = 0, next = find(s.b0, in_next);
       for (int b = s.b0; b < s.b1; ++b, ++g) {
         const int blk = next, in = in_next;
@@ -389,7 +339,6 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
           mma8<kHigh64, kHigh64>(dS, rope + ((uint32_t)slot * kRopeF8 >> 4) + (uint32_t)(kk * 2), qr + (uint32_t)(kk * 2), kIdS, 1u, el);
         mma_commit(&B.s_full[g & 1], el);
         mma_commit(&B.r_free[slot], el);
-        if (b + 1 == s.b1) mma_commit(&B.q_free, el);
         if (open && !value()) { ok = false; break; }
         open = true;
         first = b == s.b0;
@@ -424,18 +373,77 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
       return *f == 0u;
     };
     bool ok = true, any;
-    // the next tile is looked up behind the first block's weights, when these warps have time
+    // A tile's queries, a warp a row, kBatch rows at a time: 2^-e brings the largest magnitude to at most 448.  Called when
+    // this warp has seen the last tile's last scores, so no product reads the queries any more.
+    auto convert = [&](const Seg& q, float* mul) {
+      constexpr int kBatch = 4;
+#pragma unroll 1
+      for (int r0 = warp; r0 < N; r0 += kSoftWarps * kBatch) {
+        uint4 v[kBatch][3];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = r0 + k * kSoftWarps;
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(q.grow + r) * kRow);
+#pragma unroll
+          for (int m = 0; m < 3; ++m) {
+            const int c = lane + 32 * m;
+            v[k][m] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < q.nrows && c < 72) v[k][m] = __ldg(src + c);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = r0 + k * kSoftWarps;
+          if (r >= N) break;
+          uint32_t top = 0u;
+#pragma unroll
+          for (int m = 0; m < 3; ++m) {
+            top = __vmaxu2(top, __vmaxu2(v[k][m].x & 0x7fff7fffu, v[k][m].y & 0x7fff7fffu));
+            top = __vmaxu2(top, __vmaxu2(v[k][m].z & 0x7fff7fffu, v[k][m].w & 0x7fff7fffu));
+          }
+          top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
+          const int e = min(max((int)(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0), -112), 120);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+          for (int m = 0; m < 3; ++m) {
+            const int c = lane + 32 * m;
+            if (c < 72) {
+              const uint32_t w[4] = {v[k][m].x, v[k][m].y, v[k][m].z, v[k][m].w};
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float x0 = bf_lo(w[x]) * down, x1 = bf_hi(w[x]) * down;
+                hi[x] = e4m3_pair(x0, x1);
+                const float2 h = e4m3_values(hi[x]);
+                lo[x] = e4m3_pair((x0 - h.x) * 16.f, (x1 - h.y) * 16.f);
+              }
+              const uint32_t in = (uint32_t)(c & 1) * 8u;
+              const uint32_t to = c < 64 ? swz(sb + (uint32_t)(c >> 4) * C::kQSlab, r, (c & 15) >> 1)
+                                         : swz64(sb + C::kQRopeOff, r, (c - 64) >> 1);
+              st_v2(to + in, hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+              // N rows further on the swizzle is the same
+              st_v2(to + in + (c < 64 ? N * 128u : N * 64u), lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            }
+          }
+          // a query that is not finite has no finite score
+          if (lane == 0) mul[r] = top < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fffffff);
+        }
+      }
+      mbar_arrive(&B.q_full);
+    };
     Seg after;
-    bool more = walk.next(a, own, after);
+    bool more;
+    auto advance = [&]() {  // to the next tile that sees something; the others get their zeros
+      while ((more = walk.next(a, own, after)) && after.b0 >= after.b1) {
+        for (int i = st; i < after.nrows * (kVal / 8); i += kSoftThreads)
+          reinterpret_cast<uint4*>(a.out + (int64_t)after.grow * kVal)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse && st < after.nrows) a.lse[after.grow + st] = -INFINITY;
+      }
+    };
+    advance();
+    if (more) convert(after, q_mul);
     while (ok && more) {
       s = after;
-      if (s.b0 >= s.b1) {  // nothing visible
-        more = walk.next(a, own, after);
-        for (int i = st; i < s.nrows * (kVal / 8); i += kSoftThreads)
-          reinterpret_cast<uint4*>(a.out + (int64_t)s.grow * kVal)[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (a.lse && st < s.nrows) a.lse[s.grow + st] = -INFINITY;
-        continue;
-      }
       const float* qm = q_mul + (tc & 1) * N;
       if (quad == 0 && lane < NC) {
         less_max[c0 + lane] = C::kBias - kNone;
@@ -445,7 +453,6 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
       }
       dead = dead || !wait(&B.q_full, (uint32_t)tc);  // the factors
       if (!meet(false, any)) { ok = false; break; }
-      if (quad == 0 && lane == 0) mbar_arrive(&B.q_free);
       const int32_t* table = a.table + (int64_t)s.r * a.M;
       float l[NC];
 #pragma unroll
@@ -626,7 +633,7 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
         // the sums keep the weights, without the rows' scales, in fp32; behind the arrival, while the MMAs run
 #pragma unroll
         for (int c = 0; c < NC; ++c) l[c] = fmaf(v[c], unscale, l[c]);
-        if (b == s.b0) more = walk.next(a, own, after);
+        if (b == s.b0) advance();  // (while these warps have time)
       }
       if (!ok) break;
       // sums over the tokens of each row: halves of the rows change lanes until a lane has one (row lane mod NC)
@@ -658,6 +665,7 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
           a.lse[s.grow + row] = sum == 0.f ? -INFINITY : (log2f(sum) - less_max[row]) * 0.6931471805599453f;
         }
       }
+      if (more) convert(after, q_mul + ((tc + 1) & 1) * N);
       named_sync(bar_half, 128);
       dead = dead || !wait(&B.o_done, (uint32_t)tc);
       tc_after();
