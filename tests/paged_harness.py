@@ -5,8 +5,8 @@ Tolerances, from the arithmetic of the kernels (a rounding is off by at most hal
 16 bits: a weight is rounded to bf16, 2^-8 of it; 4 bits: to fp16, 2^-11, and at least 2^-32 of the running maximum's.
 8 bits: a weight W_t = w_t 2^x_t (x_t the row scale's exponent) is rounded to fp16, 2^-11, then split in two: what an E5M2
 code leaves is at most an eighth of the power of two below W, and its E4M3 code is off by at most 2^-8 of that power; below
-2^-6 codes of the rest are 2^-9 apart, off by 2^-10, where the largest weight is at least 2^9; weights below 2^-26 of the
-largest may vanish.  Queries of 8 bits are off by at most 2^-14 of a code's unit, where the row's largest is at least 224.
+2^-6 codes of the rest are 2^-9 apart, off by 2^-10, where the largest weight is at least 2^7: 2^-17 of it; E5M2 codes end at
+2^-16, so weights below 2^-24 of the largest may vanish.  Queries of 8 bits are off by at most 2^-14 of a code's unit, where the row's largest is at least 224.
 Sums of n products in fp32 that may truncate are off by n 2^-23 of the sum of magnitudes: 576 for a score (8 bits: 1152, in
 two columns, and 2^-18 for adding exponents up to 32 to a score and a maximum), the seen tokens for the weighted values and
 the sum of the weights; 2^x adds 2^-21; the output is rounded to bf16.
@@ -91,7 +91,7 @@ def check(c, q_bits, cu, kv, out, lse, scale=SCALE, window=0, sinks=0, trees=Non
                 es = 2 * es + 2.0 ** -18 + lost
                 big = w * 2.0 ** x
                 most = big.max(-1, keepdims=True, initial=0)
-                err = np.minimum(big / 8, most * 2.0 ** -19) + np.minimum(big, most * 2.0 ** -25)
+                err = np.minimum(big / 8, most * 2.0 ** -17) + np.minimum(big, most * 2.0 ** -24)
                 extra = (err * 2.0 ** -x) @ np.abs(np.where(np.isfinite(k[:, :512]), k[:, :512], 0))
             eps = {BF16: 2.0 ** -8, Q4: 2.0 ** -11, F8: 2.0 ** -8 + 2.0 ** -11}[c.fmt]
             ew = 2 * es + (count[:, None] + 8) * 2.0 ** -23

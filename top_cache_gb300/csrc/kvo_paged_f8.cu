@@ -63,8 +63,12 @@ struct ShapeF8 {
   static constexpr uint32_t kSmem = kListOff + (kOwn ? 2400 : 0);
   static constexpr uint32_t kTmem = 8 * N;                 // O^T 4 N columns, then S^T twice 2 N
   static constexpr uint32_t kColS = 4 * N;
-  static constexpr float kBias = 9.f;                      // log2 of the largest weight when the running maximum has moved;
-  static constexpr float kRescale = 2.f;                   // it may grow by 2^2: lo ends at 448, an eighth of 2^11.8
+  // log2 of the largest weight when the running maximum has moved, and how far a score may pass it: lo ends at 448, an eighth
+  // of 2^11.8.  9 and 2 keep more of small weights (hi ends 2^-26 below the largest, not 2^-24) but move the maximum more
+  // often, 4,000 clocks each: 16 x 4 positions of 128 heads over 8k 79 us for 76, a windowed chunk of 2,048 tokens 191 for
+  // 177, 32 trees of 64 nodes over 16k 528 for 504.
+  static constexpr float kBias = 7.f;
+  static constexpr float kRescale = 4.f;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
   static_assert(kRingOff % 1024 == 0 && kRopeOff % 1024 == 0 && kPOff % 1024 == 0 && kBarOff % 8 == 0,
                 "swizzled tiles sit on 1 KB boundaries");
@@ -116,13 +120,6 @@ __device__ __forceinline__ void tma_rope(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(0), "r"(row), "r"(block), "r"(smem_u32(bar))
       : "memory");
 }
-// Two values to E4M3 codes (low byte: x), nearest even, saturating.
-__device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 e4m3_values(uint32_t two) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
-}
 // Two weights -> hi + lo: the E5M2 code is the high byte of fp16, rounded to nearest; what is left goes to E4M3.
 // hi: bytes 1 and 3; lo: the low 16 bits.  A NaN is one in lo.
 __device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -131,6 +128,15 @@ __device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, ui
   hi = (b + 0x00800080u) & 0xff00ff00u;
   const __half2 rest = __hsub2(h, *reinterpret_cast<const __half2*>(&hi));
   lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(rest), __NV_SATFINITE, __NV_E4M3);
+}
+
+// A load where `on`, else `other`, issued where it stands (an ordinary one is moved down to its use, a block later) and
+// without a branch (whose end waits for it).
+__device__ __forceinline__ uint32_t load_if(bool on, const void* p, uint32_t other) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q ld.global.nc.b32 %0, [%1];\n\t}"
+               : "+r"(other)
+               : "l"(p), "r"((uint32_t)on));
+  return other;
 }
 
 struct BarsF8 {
@@ -245,8 +251,11 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
       for (int b = s.b0; b < s.b1; ++b, ++g) {
         const int blk = next, in = in_next;
         next = find(b + 1, in_next);
-        if (next >= 0)  // half of the run's rows
-          prefetch_l2(a.pool + next * block_bytes + ((int64_t)in_next + (lane >> 4) * (run / 2)) * kRow, (uint32_t)(run / 2) * kRow);
+        if (next >= 0) {  // half of the run's rows, and its scales (which the softmax warps load one by one)
+          const uint8_t* block = a.pool + next * block_bytes;
+          prefetch_l2(block + ((int64_t)in_next + (lane >> 4) * (run / 2)) * kRow, (uint32_t)(run / 2) * kRow);
+          if (lane < 16) prefetch_l2(block + (int64_t)a.B * kRow + 4 * in_next, (uint32_t)run * 4);
+        }
         const uint32_t got = __popc(__ballot_sync(kFull, blk >= 0)) >> 1;  // runs
         const uint32_t off = (uint32_t)((lane & 15) * run);
 #pragma unroll
@@ -277,7 +286,8 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
       landed = phase_wait(&B.r_full[x % C::kRopes], (uint32_t)(x / C::kRopes) & 1u, a.wait_ns) && landed;
     if (!landed) fail();
   } else if (warp == kMmaWarp) {
-    // ---- MMA issue: S^T of a block, then O^T of the one before it -----------------------------
+    // ---- MMA issue: S^T of a block, then O^T of the one before it; a tile's last O^T at once, since the next tile's
+    // queries come behind its last weights ----------------------------------------------------------
     // The proxy fences stand here, behind the waits, for the bytes that other threads wrote with ordinary stores.
     const uint32_t el = elect();
     constexpr uint32_t kIdS = idesc8(false, 2 * N, false, false);
@@ -346,9 +356,10 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
         og = g;
         otc = tc;
       }
+      if (ok) ok = value();
+      open = false;
       ++tc;
     }
-    if (ok && open) ok = value();
     if (!ok) fail();
     // everything issued is complete before TMEM is freed (the tensor pipe waits on nothing outside this CTA)
     mma_commit(&B.fin, el);
@@ -373,60 +384,70 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
       return *f == 0u;
     };
     bool ok = true, any;
-    // A tile's queries, a warp a row, kBatch rows at a time: 2^-e brings the largest magnitude to at most 448.  Called when
-    // this warp has seen the last tile's last scores, so no product reads the queries any more.
+    // A tile's queries: 2^-e brings a row's largest magnitude to at most 448.  A warp has N / 8 rows side by side, up to
+    // four at a time: their 16-byte pieces in a line, 72 a row.  Called when this warp has seen the last tile's last scores,
+    // so no product reads the queries any more.
     auto convert = [&](const Seg& q, float* mul) {
-      constexpr int kBatch = 4;
+      constexpr int kRows = N / kSoftWarps, kAt = kRows < 4 ? kRows : 4, kSteps = (kAt * 72 + 31) / 32, kTurns = kRows / kAt;
 #pragma unroll 1
-      for (int r0 = warp; r0 < N; r0 += kSoftWarps * kBatch) {
-        uint4 v[kBatch][3];
+      for (int turn = 0; turn < kTurns; ++turn) {
+        const int r0 = warp * kRows + turn * kAt, pieces = min(max(q.nrows - r0, 0), kAt) * 72;  // (rows behind the tile's: zeros)
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(q.grow + r0) * kRow);
+        uint4 v[kSteps];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = r0 + k * kSoftWarps;
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(q.grow + r) * kRow);
+        for (int m = 0; m < kSteps; ++m) {
+          v[m] = make_uint4(0u, 0u, 0u, 0u);
+          if (32 * m + lane < pieces) v[m] = __ldg(src + 32 * m + lane);
+        }
+        uint32_t top[kAt];
 #pragma unroll
-          for (int m = 0; m < 3; ++m) {
-            const int c = lane + 32 * m;
-            v[k][m] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < q.nrows && c < 72) v[k][m] = __ldg(src + c);
+        for (int k = 0; k < kAt; ++k) top[k] = 0u;
+#pragma unroll
+        for (int m = 0; m < kSteps; ++m) {
+          const uint32_t most = __vmaxu2(__vmaxu2(v[m].x & 0x7fff7fffu, v[m].y & 0x7fff7fffu),
+                                         __vmaxu2(v[m].z & 0x7fff7fffu, v[m].w & 0x7fff7fffu));
+          const int first = 32 * m / 72, last = (32 * m + 31) / 72;  // the step's rows, one or two
+          const bool second = 32 * m + lane >= 72 * last;
+          if (first == last) {
+            if (first < kAt) top[first] = __vmaxu2(top[first], most);
+          } else {
+            top[first] = __vmaxu2(top[first], second ? 0u : most);
+            if (last < kAt) top[last] = __vmaxu2(top[last], second ? most : 0u);
           }
         }
+        float down[kAt];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = r0 + k * kSoftWarps;
-          if (r >= N) break;
-          uint32_t top = 0u;
-#pragma unroll
-          for (int m = 0; m < 3; ++m) {
-            top = __vmaxu2(top, __vmaxu2(v[k][m].x & 0x7fff7fffu, v[k][m].y & 0x7fff7fffu));
-            top = __vmaxu2(top, __vmaxu2(v[k][m].z & 0x7fff7fffu, v[k][m].w & 0x7fff7fffu));
-          }
-          top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
-          const int e = min(max((int)(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0), -112), 120);
-          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-          for (int m = 0; m < 3; ++m) {
-            const int c = lane + 32 * m;
-            if (c < 72) {
-              const uint32_t w[4] = {v[k][m].x, v[k][m].y, v[k][m].z, v[k][m].w};
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float x0 = bf_lo(w[x]) * down, x1 = bf_hi(w[x]) * down;
-                hi[x] = e4m3_pair(x0, x1);
-                const float2 h = e4m3_values(hi[x]);
-                lo[x] = e4m3_pair((x0 - h.x) * 16.f, (x1 - h.y) * 16.f);
-              }
-              const uint32_t in = (uint32_t)(c & 1) * 8u;
-              const uint32_t to = c < 64 ? swz(sb + (uint32_t)(c >> 4) * C::kQSlab, r, (c & 15) >> 1)
-                                         : swz64(sb + C::kQRopeOff, r, (c - 64) >> 1);
-              st_v2(to + in, hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-              // N rows further on the swizzle is the same
-              st_v2(to + in + (c < 64 ? N * 128u : N * 64u), lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            }
-          }
+        for (int k = 0; k < kAt; ++k) {
+          const uint32_t most = __reduce_max_sync(kFull, max(top[k] & 0xffffu, top[k] >> 16));
+          const int e = min(max((int)(most >> 7) - 127 - 8 + ((most & 127u) > 96u ? 1 : 0), -112), 120);
+          down[k] = __uint_as_float((uint32_t)(127 - e) << 23);
           // a query that is not finite has no finite score
-          if (lane == 0) mul[r] = top < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fffffff);
+          if (lane == 0)
+            mul[r0 + k] = most < 0x7f80u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fffffff);
+        }
+#pragma unroll
+        for (int m = 0; m < kSteps; ++m) {
+          const int i = 32 * m + lane, first = 32 * m / 72, last = (32 * m + 31) / 72;
+          const bool second = first != last && i >= 72 * last;
+          if (second && last >= kAt) continue;
+          const float by = second && last < kAt ? down[last < kAt ? last : 0] : down[first];
+          const int row = second ? last : first, c = i - 72 * row, r = r0 + row;
+          const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            // (8 bits up to 448 are exact in fp16, down to where they pass the codes' range)
+            const __half2 h = __floats2half2_rn(bf_lo(w[x]) * by, bf_hi(w[x]) * by);
+            hi[x] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(h), __NV_SATFINITE, __NV_E4M3);
+            const __half2 rest = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[x], __NV_E4M3)));
+            lo[x] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(__hmul2(rest, __float2half2_rn(16.f))), __NV_SATFINITE, __NV_E4M3);
+          }
+          const uint32_t in = (uint32_t)(c & 1) * 8u;
+          const uint32_t to = c < 64 ? swz(sb + (uint32_t)(c >> 4) * C::kQSlab, r, (c & 15) >> 1)
+                                     : swz64(sb + C::kQRopeOff, r, (c - 64) >> 1);
+          st_v2(to + in, hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          // N rows further on the swizzle is the same
+          st_v2(to + in + (c < 64 ? N * 128u : N * 64u), lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         }
       }
       mbar_arrive(&B.q_full);
@@ -445,6 +466,19 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
     while (ok && more) {
       s = after;
       const float* qm = q_mul + (tc & 1) * N;
+      const int32_t* table = a.table + (int64_t)s.r * a.M;
+      // the cache block of this thread's token of block b (-1: no position's), and its row's scale
+      auto entry = [&](int b) -> int32_t {
+        const int t = s.block(b) * kBlk + tok;
+        return (int32_t)load_if(b < s.b1 && s.any_sees(a, t), table + entry_of(a, t), 0xffffffffu);
+      };
+      auto there = [&](int32_t blk) -> bool { return blk >= 0 && (int64_t)blk < a.n_blocks; };
+      auto scale_of = [&](int b, int32_t blk) -> uint32_t {
+        const int t = s.block(b) * kBlk + tok;
+        return load_if(there(blk), a.pool + blk * block_bytes + (int64_t)a.B * kRow + 4 * (t - entry_of(a, t) * a.B), 0x3f800000u);
+      };
+      int32_t blk_next = entry(s.b0), blk_far = entry(s.b0 + 1);
+      uint32_t bits_next;
       if (quad == 0 && lane < NC) {
         less_max[c0 + lane] = C::kBias - kNone;
         const int i = (s.row0 + min(c0 + lane, s.nrows - 1)) / a.H;  // the row's query token
@@ -453,27 +487,17 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
       }
       dead = dead || !wait(&B.q_full, (uint32_t)tc);  // the factors
       if (!meet(false, any)) { ok = false; break; }
-      const int32_t* table = a.table + (int64_t)s.r * a.M;
       float l[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) l[c] = 0.f;
-      // whether block b's token is there for any position, and its row's scale
-      auto mapped = [&](int b, uint32_t& bits) -> bool {
-        const int t = s.block(b) * kBlk + tok;
-        bits = 0x3f800000u;
-        if (b >= s.b1 || !s.any_sees(a, t)) return false;
-        const int j = entry_of(a, t);
-        const int32_t blk = __ldg(table + j);
-        if (blk < 0 || (int64_t)blk >= a.n_blocks) return false;
-        bits = __ldg(reinterpret_cast<const uint32_t*>(a.pool + blk * block_bytes + (int64_t)a.B * kRow) + (t - j * a.B));
-        return true;
-      };
-      uint32_t bits_next;
-      bool here_next = mapped(s.b0, bits_next);
+      bits_next = scale_of(s.b0, blk_next);
       for (int b = s.b0; b < s.b1; ++b, ++g) {
-        const bool here = here_next;
+        // loads run ahead: the next block's scale, the table's entry of the one behind it
+        const bool here = there(blk_next);
         const uint32_t bits = bits_next;
-        here_next = mapped(b + 1, bits_next);
+        blk_next = blk_far;
+        bits_next = scale_of(b + 1, blk_next);
+        blk_far = entry(b + 2);
         // the scale 2^x, or NaN, which then is the score's; x and 2^-x are finite either way
         const bool fine = row_scale_valid(bits);
         const float scale = fine ? __uint_as_float(bits) : __int_as_float(0x7fffffff);
@@ -504,7 +528,7 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
         const uint32_t sS = tmem + lane_addr + C::kColS + (uint32_t)(g & 1) * (2 * N) + (uint32_t)c0;
         float v[NC];
         bool odd = false;  // the row has a code that is not a number
-        // v: the raw scores times the row's scale
+        // v: the raw scores
         auto raw = [&]() {
           float lo[NC];
           tmem_ld<NC>(sS, v);
@@ -512,17 +536,27 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
           tmem_wait_ld();
           odd = !(fabsf(v[0]) < INFINITY);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) v[c] = fmaf(lo[c], 0.0625f, v[c]) * scale;
+          for (int c = 0; c < NC; c += 2) {
+            const float2 y = __ffma2_rn(make_float2(lo[c], lo[c + 1]), make_float2(0.0625f, 0.0625f), make_float2(v[c], v[c + 1]));
+            v[c] = y.x;
+            v[c + 1] = y.y;
+          }
         };
         raw();
-        // log2 of the weights: v, in log2 units, plus x, less the running maximum (plus kBias); -inf where hidden
+        // log2 of the weights: v times the row's scale, in log2 units, plus x, less the running maximum (plus kBias); -inf
+        // where hidden
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
           const float4 y = *reinterpret_cast<const float4*>(qm + c0 + c), m = *reinterpret_cast<const float4*>(less_max + c0 + c);
-          v[c] = fmaf(v[c], y.x, m.x + x);
-          v[c + 1] = fmaf(v[c + 1], y.y, m.y + x);
-          v[c + 2] = fmaf(v[c + 2], y.z, m.z + x);
-          v[c + 3] = fmaf(v[c + 3], y.w, m.w + x);
+          const float2 by = make_float2(scale, scale), more_x = make_float2(x, x);
+          const float2 p = __ffma2_rn(make_float2(v[c], v[c + 1]), __fmul2_rn(make_float2(y.x, y.y), by),
+                                      __fadd2_rn(make_float2(m.x, m.y), more_x));
+          const float2 q = __ffma2_rn(make_float2(v[c + 2], v[c + 3]), __fmul2_rn(make_float2(y.z, y.w), by),
+                                      __fadd2_rn(make_float2(m.z, m.w), more_x));
+          v[c] = p.x;
+          v[c + 1] = p.y;
+          v[c + 2] = q.x;
+          v[c + 3] = q.y;
         }
         if (!plain) {
 #pragma unroll
@@ -541,7 +575,7 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
           int32_t mine = 0;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            v[c] = (vis >> c) & 1u ? __fadd_rn(__fmul_rn(v[c], qm[c0 + c]), x) : -INFINITY;
+            v[c] = (vis >> c) & 1u ? __fadd_rn(__fmul_rn(v[c], qm[c0 + c] * scale), x) : -INFINITY;
             const int32_t w = __reduce_max_sync(kFull, as_ordered(v[c]));
             if (lane == c) mine = w;
           }
@@ -632,7 +666,11 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
         mbar_arrive(&B.p_full);
         // the sums keep the weights, without the rows' scales, in fp32; behind the arrival, while the MMAs run
 #pragma unroll
-        for (int c = 0; c < NC; ++c) l[c] = fmaf(v[c], unscale, l[c]);
+        for (int c = 0; c < NC; c += 2) {
+          const float2 y = __ffma2_rn(make_float2(v[c], v[c + 1]), make_float2(unscale, unscale), make_float2(l[c], l[c + 1]));
+          l[c] = y.x;
+          l[c + 1] = y.y;
+        }
         if (b == s.b0) advance();  // (while these warps have time)
       }
       if (!ok) break;
