@@ -213,11 +213,11 @@ __global__ void __launch_bounds__(kCommitThreads) commit_paged_kernel(CommitArgs
 }
 
 // ---------------------------------------------------------------------------
-// move: a CTA a request and pool; a thread has one piece of every row (16 bytes
-// of codes, 4 of scales).  The path's nodes ascend and node path[k] lies at or
-// behind place k, so rows go forward only: a batch's sources are read before its
-// places are written, and no place of it is a later batch's source.  Threads
-// share no bytes.
+// move: a CTA a request and pool.  Where the rows lie is found for many of them
+// at once; then a thread has one piece of every row (16 bytes of codes, 4 of
+// scales).  The path's nodes ascend and node path[k] lies at or behind place k,
+// so rows go forward only: a batch's sources are read before its places are
+// written, and no place of it is a later batch's source.  Threads share no bytes.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 96;  // 72 pieces of a bf16 row; 37 of 8 bits; 27 of 4
 constexpr int kMoveBatch = 8;
@@ -235,47 +235,53 @@ __global__ void __launch_bounds__(kMoveThreads) move_paged_kernel(MoveArgs a) {
   if (!nodes_of(a.cu, r, a.n_tokens, first, n)) return;
   const int kv = a.kv_lens[r], count = min(a.accepted[r], n);
   if (count <= 0 || kv < n || (int64_t)kv > (int64_t)a.M * a.B) return;
+  __shared__ int4 rows[kMoveThreads];  // from: cache block (-1: none moves), row in it; to
   const int before = kv - n, tid = threadIdx.x;
   const int wide = a.row_bytes / 16, narrow = a.scale_bytes / 4;
-  const bool is_wide = tid < wide;
-  if (tid >= wide + narrow) return;
+  const bool is_wide = tid < wide, mine = tid < wide + narrow;
   const int64_t block_bytes = (int64_t)a.B * (a.row_bytes + a.scale_bytes);
   const int32_t* table = a.table + (int64_t)r * a.M;
   uint8_t* pool = a.pools + (int64_t)blockIdx.y * a.stride;
-  auto piece = [&](int t) -> uint8_t* {  // this thread's piece of token t's row; null: not mapped
-    const int j = t / a.B, in = t - j * a.B;
-    const int32_t b = __ldg(table + j);
-    if (b < 0 || (int64_t)b >= a.n_blocks) return nullptr;
-    uint8_t* base = pool + b * block_bytes;
+  auto piece = [&](int blk, int in) -> uint8_t* {  // this thread's piece of a row
+    uint8_t* base = pool + blk * block_bytes;
     return is_wide ? base + (int64_t)in * a.row_bytes + 16 * tid
                    : base + (int64_t)a.B * a.row_bytes + (int64_t)in * a.scale_bytes + 4 * (tid - wide);
   };
-  for (int k0 = 0; k0 < count; k0 += kMoveBatch) {
-    uint4 v[kMoveBatch];
-    uint8_t* dst[kMoveBatch];
+  for (int k0 = 0; k0 < count; k0 += kMoveThreads) {
+    const int k = k0 + tid;
+    int4 row = make_int4(-1, 0, 0, 0);
+    const int p = k < count ? __ldg(a.path + first + k) : -1;
+    if (p > k && p < n) {
+      const int s = (before + p) / a.B, d = (before + k) / a.B;
+      const int32_t bs = __ldg(table + s), bd = __ldg(table + d);
+      if (bs >= 0 && (int64_t)bs < a.n_blocks && bd >= 0 && (int64_t)bd < a.n_blocks)
+        row = make_int4(bs, before + p - s * a.B, bd, before + k - d * a.B);
+    }
+    rows[tid] = row;
+    __syncthreads();
+    const int some = min(kMoveThreads, count - k0);
+    for (int j = 0; mine && j < some; j += kMoveBatch) {
+      uint4 v[kMoveBatch];
 #pragma unroll
-    for (int k = 0; k < kMoveBatch; ++k) {
-      dst[k] = nullptr;
-      const int p = k0 + k < count ? __ldg(a.path + first + k0 + k) : -1;
-      if (p > k0 + k && p < n) {
-        const uint8_t* src = piece(before + p);
-        if (src) {
-          dst[k] = piece(before + k0 + k);
-          if (is_wide)
-            v[k] = *reinterpret_cast<const uint4*>(src);
-          else
-            v[k].x = *reinterpret_cast<const uint32_t*>(src);
-        }
+      for (int i = 0; i < kMoveBatch; ++i) {
+        if (j + i >= some || rows[j + i].x < 0) continue;
+        const uint8_t* src = piece(rows[j + i].x, rows[j + i].y);
+        if (is_wide)
+          v[i] = *reinterpret_cast<const uint4*>(src);
+        else
+          v[i].x = *reinterpret_cast<const uint32_t*>(src);
+      }
+#pragma unroll
+      for (int i = 0; i < kMoveBatch; ++i) {
+        if (j + i >= some || rows[j + i].x < 0) continue;
+        uint8_t* dst = piece(rows[j + i].z, rows[j + i].w);
+        if (is_wide)
+          *reinterpret_cast<uint4*>(dst) = v[i];
+        else
+          *reinterpret_cast<uint32_t*>(dst) = v[i].x;
       }
     }
-#pragma unroll
-    for (int k = 0; k < kMoveBatch; ++k) {
-      if (!dst[k]) continue;
-      if (is_wide)
-        *reinterpret_cast<uint4*>(dst[k]) = v[k];
-      else
-        *reinterpret_cast<uint32_t*>(dst[k]) = v[k].x;
-    }
+    __syncthreads();
   }
 }
 
