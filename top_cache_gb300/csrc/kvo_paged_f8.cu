@@ -17,6 +17,32 @@
 //            sum that divides is of P' / t in fp32.
 // A product of E4M3 and E4M3 or E5M2 with fp32 sums is exact but for the sums'
 // truncation (measured: 2^-22 of the sum of magnitudes).
+//
+// One persistent CTA per SM: 8 softmax warps (which also split the next tile's
+// queries, as soon as this one's scores are done), a copy warp and an MMA warp.
+// The ring has 4 pairs of slabs (two blocks) at N = 64 and 5 below.  S^T has two
+// places in TMEM: the next block's is issued before this one's O^T, so that the
+// softmax of one block runs beside the products of another.  Every wait is
+// bounded, as there.
+//
+// What bounds it.  N = 16: HBM, 32 ragged requests of 64k, 16 heads, in 136 us
+// (6.4 TB/s, 0.93 of the copy rate; with what joins them 143).  The cache's bytes
+// are all it reads (ncu: 863 of 862 MB).  Two loads a token stand in the way, its
+// table entry and its scale: they are made two blocks and one block ahead and
+// the scales are fetched into L2 with the codes (157 us before).  N = 64: 4,200
+// clocks a block of 128 tokens, where the products take 1,200 (S^T, 18 of 64 to 78
+// clocks) and 1,600 to 2,200 (O^T, 32 of 50 to 69) and the softmax 3,300 beside
+// them; each waits a few hundred for the other.  The 16-bit kernel takes 4,800 and
+// the 4-bit one 6,200.  Borders of tiles cost 10,000: the queries 3,000 to 4,000,
+// the output or the parts 4,000 to 6,000 (64 rows of 2 KB).
+// Tried and not faster: four warps of their own for the queries (a latency of
+// memory a row: 106 us for 82 over 16 x 4 positions of 128 heads of 8k), votes on
+// the running maximum counted behind the weights (73 for 70), 32 columns of TMEM a
+// load, all of a tile's queries loaded before any is split (76 for 71), one arrival a
+// warp at the barriers.
+// Tiles, us with N = 16, 32, 64: 16 requests of 32k and 16 rows 66, 76, 87; 24 rows
+// 109, 78, 89; 48 rows 157, 120, 91; 128 rows 364, 211, 156: the rule of the other
+// formats holds.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
@@ -161,8 +187,11 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
   constexpr int NC = C::kNC;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
-  if (sb & 1023u) {  // there is no room to align it here
-    if (threadIdx.x == 0) atomicOr(a.status, kErrPlan);
+  if (sb & 1023u) {  // there is no room to align it here: nothing is computed, and nothing joined
+    if (threadIdx.x == 0 && blockIdx.x == 0) {
+      *a.status = kErrPlan;
+      a.head[kHdListed] = 0;
+    }
     return;
   }
   float* less_max = reinterpret_cast<float*>(smem + C::kMiscOff);      // [N] kBias - running maximum (log2 units)
@@ -492,17 +521,18 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
       for (int c = 0; c < NC; ++c) l[c] = 0.f;
       bits_next = scale_of(s.b0, blk_next);
       for (int b = s.b0; b < s.b1; ++b, ++g) {
-        // loads run ahead: the next block's scale, the table's entry of the one behind it
+        // the scale 2^x, or NaN, which then is the score's; x and 2^-x are finite either way
         const bool here = there(blk_next);
         const uint32_t bits = bits_next;
-        blk_next = blk_far;
-        bits_next = scale_of(b + 1, blk_next);
-        blk_far = entry(b + 2);
-        // the scale 2^x, or NaN, which then is the score's; x and 2^-x are finite either way
         const bool fine = row_scale_valid(bits);
         const float scale = fine ? __uint_as_float(bits) : __int_as_float(0x7fffffff);
         const float x = fine ? (float)((int)(bits >> 23) - 127) : 0.f;
         const float unscale = fine ? __uint_as_float((254u << 23) - bits) : 1.f;
+        asm volatile("" ::"f"(scale), "f"(x), "f"(unscale));  // before the loads, or their arrival is waited for too
+        // loads run ahead: the next block's scale, the table's entry of the one behind it
+        blk_next = blk_far;
+        bits_next = scale_of(b + 1, blk_next);
+        blk_far = entry(b + 2);
         const int t = s.block(b) * kBlk + tok;
         // the token is seen by every position of the tile, or by some
         const bool all = here && t <= s.pmin && (a.window == 0 || t > s.pmax - a.window || t < a.sinks);

