@@ -479,7 +479,9 @@ int64_t kvo_paged_block_bytes(int32_t format, int32_t block_tokens);
  *                 block is at or below new length - window, and at or past
  *                 block ceil(sinks / block_tokens)).  Their table entries stay
  *                 and must not be read past the step's own positions.  The same
- *                 window and sinks in every call of a request.  0: none.
+ *                 window and sinks in every call of a request (but a step of draft
+ *                 trees plans with window 0 and gives blocks up in kvo_paged_commit).
+ *                 0: none.
  *   lengths_out : device int32 [n_requests], may be lengths: the new length, 0
  *                 for an ended request
  *   kv_lens     : device int32 [n_requests]: the new length, 0 for a refused

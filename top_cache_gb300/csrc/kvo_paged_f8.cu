@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
   const int64_t block_bytes = (int64_t)a.B * kRowBytesF8;
 
   if (warp == kCopyWarp) {
-    // ---- copies: lanes l and l + 16 hold the cache block and row of a block's run l (-1: not read): of this block, and of
-    // the next one, which is already on its way into L2 ----------------------------------------
+    // ---- copies: lane l < 16 (and l + 16) holds the cache block and row of a block's run l (-1: not read): of this block,
+    // and of the next one --------------------------------------------------------------------------
     const int run = maps.run, runs = kBlk / run;
     int pairs = 0;  // filled, or being filled
     bool ok = true;
@@ -280,10 +280,15 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
       for (int b = s.b0; b < s.b1; ++b, ++g) {
         const int blk = next, in = in_next;
         next = find(b + 1, in_next);
-        if (next >= 0) {  // half of the run's rows, and its scales (which the softmax warps load one by one)
+        // The next block into L2, with its scales, which the softmax warps load one by one.  Runs of 8 rows keep the copy
+        // unit busy with boxes (three a run) as it is.  32 requests of 32k, 16 heads, us with none, the scales, all in one or
+        // two requests, all in two or three: blocks of 8 tokens 143, 154, 154, 191; of 24 145, 157, 177, 196; of 16 130, 136,
+        // 117, 128; of 64 126, 126, 109, 110.
+        if (run > 8 && next >= 0 && lane < 16) {
           const uint8_t* block = a.pool + next * block_bytes;
-          prefetch_l2(block + ((int64_t)in_next + (lane >> 4) * (run / 2)) * kRow, (uint32_t)(run / 2) * kRow);
-          if (lane < 16) prefetch_l2(block + (int64_t)a.B * kRow + 4 * in_next, (uint32_t)run * 4);
+          const bool joint = run == a.B;  // they lie behind the run
+          prefetch_l2(block + (int64_t)in_next * kRow, (uint32_t)run * (joint ? kRowBytesF8 : kRow));
+          if (!joint) prefetch_l2(block + (int64_t)a.B * kRow + 4 * in_next, (uint32_t)run * 4);
         }
         const uint32_t got = __popc(__ballot_sync(kFull, blk >= 0)) >> 1;  // runs
         const uint32_t off = (uint32_t)((lane & 15) * run);
