@@ -560,8 +560,9 @@ int kvo_paged_read(const void* pool, int64_t n_blocks, int32_t block_tokens, int
  * Precision: scores and sums in fp32 on exact products (KVO_CACHE_Q4: a query
  * element more than 2^31 below its row's largest loses bits; KVO_CACHE_F8: one more
  * than 2^14 below); the softmax weights of the value product are rounded to bf16
- * (KVO_CACHE_Q4: fp16; KVO_CACHE_F8: times their rows' scales, to as many bits as
- * bf16 has in two terms, and to fewer below 2^-10 of the largest), their sum is not;
+ * (KVO_CACHE_Q4: fp16, or 2^-32 of the row's largest; KVO_CACHE_F8: times
+ * their rows' scales, off by at most 2^-8 of themselves or 2^-28 of the row's largest,
+ * whichever is more), their sum is not;
  * out is rounded to bf16.  The same inputs give the same bits.
  * A cached element that is not finite reaches only positions that see its row:
  * they get NaN, or, where the row's score is -infinity, may get what they would

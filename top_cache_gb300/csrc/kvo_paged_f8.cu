@@ -11,10 +11,18 @@
 //            row's largest.  hi and lo are 2 N columns of one product; the
 //            scores are D_hi + D_lo / 16, times 2^e and the token's scale.
 //   weights  the token's scale t = 2^x goes into the weight: P' = 2^(s + x - m'),
-//            m' the running maximum of s + x.  P' = hi + lo, hi E5M2 (its range
-//            reaches 2^-16), lo E4M3, both to nearest: off by at most 2^-8 of
-//            P', as a bf16 weight is.  Both products add to the same O^T.  The
-//            sum that divides is of P' / t in fp32.
+//            m' the running maximum of s + x.  P' is rounded to fp16 and split
+//            into three E5M2 codes, each the nearest to what the ones before
+//            leave: together off by at most 2^-10 of P', where a bf16 weight is
+//            off by 2^-8.  E5M2 for its range: E4M3 codes of the rest, one bit
+//            finer, end 2^-17 below the largest weight, and the weights that
+//            share what an attention sink leaves lie there (2^-14 of the sink's:
+//            outputs off by 3 %).  At N = 16 and 32 the codes are 3 N columns of
+//            one product, with sums of their own, and count 1, 2^-4 and 2^-8:
+//            2^-8 of a weight down to 2^-26 of the largest.  At N = 64 TMEM has
+//            room for one set of sums, which take all three products: 2^-8 down
+//            to 2^-20 of the largest, and nothing is off by more than 2^-28 of
+//            it.  The sum that divides is of P' / t in fp32.
 // A product of E4M3 and E4M3 or E5M2 with fp32 sums is exact but for the sums'
 // truncation (measured: 2^-22 of the sum of magnitudes).
 //
@@ -22,26 +30,30 @@
 // queries, as soon as this one's scores are done), a copy warp and an MMA warp.
 // The ring has 4 pairs of slabs (two blocks) at N = 64 and 5 below.  S^T has two
 // places in TMEM: the next block's is issued before this one's O^T, so that the
-// softmax of one block runs beside the products of another.  Every wait is
-// bounded, as there.
+// softmax of one block runs beside the products of another.  At N = 64 shared
+// memory has no room for the third codes: they lie where the next block's rope
+// keys have been, between its S^T and their part of O^T, and come behind an
+// arrival of their own while the first two run (596 us over 32 trees of 64 nodes of
+// 16k; behind one arrival 638).  Every wait is bounded, as there.
 //
 // What bounds it.  N = 16: HBM, 32 ragged requests of 64k, 16 heads, in 136 us
 // (6.4 TB/s, 0.93 of the copy rate; with what joins them 143).  The cache's bytes
 // are all it reads (ncu: 863 of 862 MB).  Two loads a token stand in the way, its
 // table entry and its scale: they are made two blocks and one block ahead and
-// the scales are fetched into L2 with the codes (157 us before).  N = 64: 4,200
-// clocks a block of 128 tokens, where the products take 1,200 (S^T, 18 of 64 to 78
-// clocks) and 1,600 to 2,200 (O^T, 32 of 50 to 69) and the softmax 3,300 beside
-// them; each waits a few hundred for the other.  The 16-bit kernel takes 4,800 and
-// the 4-bit one 6,200.  Borders of tiles cost 10,000: the queries 3,000 to 4,000,
-// the output or the parts 4,000 to 6,000 (64 rows of 2 KB).
+// the scales are fetched into L2 with the codes (157 us before).  N = 64: 4,900
+// clocks a block of 128 tokens.  The products take 1,200 (S^T, 18 of 64 to 78
+// clocks) and 2,400 to 3,300 (O^T, 48 of 50 to 69), and the next block's last slabs
+// and rope keys come some 900 after the last of them; the softmax, 3,500, runs
+// beside.  (With two codes 4,200.  The 16-bit kernel takes 4,800 and the 4-bit one
+// 6,200.)  Borders of tiles cost 10,000: the queries 3,000 to 4,000, the output or
+// the parts 4,000 to 6,000 (64 rows of 2 KB).
 // Tried and not faster: four warps of their own for the queries (a latency of
 // memory a row: 106 us for 82 over 16 x 4 positions of 128 heads of 8k), votes on
 // the running maximum counted behind the weights (73 for 70), 32 columns of TMEM a
 // load, all of a tile's queries loaded before any is split (76 for 71), one arrival a
-// warp at the barriers.
-// Tiles, us with N = 16, 32, 64: 16 requests of 32k and 16 rows 66, 76, 87; 24 rows
-// 109, 78, 89; 48 rows 157, 120, 91; 128 rows 364, 211, 156: the rule of the other
+// warp at the barriers.  (Figures of the two-code kernel.)
+// Tiles, us with N = 16, 32, 64: 16 requests of 32k and 16 rows 65, 73, 101; 24 rows
+// 107, 74, 103; 48 rows 153, 116, 104; 128 rows 356, 200, 174: the rule of the other
 // formats holds.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -71,30 +83,33 @@ template <int N>
 struct ShapeF8 {
   static constexpr int kThreads = kSoftThreads + 64;
   static constexpr int kNC = N / 2;                        // rows of one softmax thread
+  static constexpr bool kApart = N != 64;                  // the three codes of a weight have sums of their own in TMEM
   static constexpr int kRing = N == 64 ? 4 : kMaxPairs;    // pairs
-  static constexpr int kRopes = N == 64 ? 1 : N == 32 ? 2 : kMaxRopes;
+  static constexpr int kRopes = N == 16 ? kMaxRopes : 1;
   static constexpr bool kOwn = N != 64;                    // room for a list of its own
   static constexpr uint32_t kQSlab = 2 * N * 128;          // hi rows, lo rows
   static constexpr uint32_t kQRopeOff = 4 * kQSlab;
   static constexpr uint32_t kRingOff = kQRopeOff + 2 * N * 64;
   static constexpr uint32_t kRopeOff = kRingOff + kRing * kPairF8;
   static constexpr uint32_t kPOff = kRopeOff + kRopes * kRopeF8;
-  static constexpr uint32_t kPHalf = N * 128;              // hi, then lo
-  static constexpr uint32_t kMiscOff = kPOff + 2 * kPHalf;
+  static constexpr uint32_t kPPart = N * 128;              // a code of every weight: hi, mid and lo
+  static constexpr uint32_t kLastOff = kApart ? kPOff + 2 * kPPart : kRopeOff;  // lo; N = 64: in the rope keys' place
+  static constexpr uint32_t kMiscOff = kPOff + (kApart ? 3 : 2) * kPPart;
   // misc: less running maxima, row positions, a tree's nodes [N], query factors [2][N], factors of a move of the running
   // maximum or 1 / l [N], a block's maxima or the tile's sums [8][NC]
   static constexpr uint32_t kMiscBytes = (6 * N + 8 * kNC) * 4;
   static constexpr uint32_t kBarOff = kMiscOff + kMiscBytes;
   static constexpr uint32_t kListOff = kBarOff + 256;
   static constexpr uint32_t kSmem = kListOff + (kOwn ? 2400 : 0);
-  static constexpr uint32_t kTmem = 8 * N;                 // O^T 4 N columns, then S^T twice 2 N
-  static constexpr uint32_t kColS = 4 * N;
-  // log2 of the largest weight when the running maximum has moved, and how far a score may pass it: lo ends at 448, an eighth
-  // of 2^11.8.  9 and 2 keep more of small weights (hi ends 2^-26 below the largest, not 2^-24) but move the maximum more
-  // often, 4,000 clocks each: 16 x 4 positions of 128 heads over 8k 79 us for 76, a windowed chunk of 2,048 tokens 191 for
-  // 177, 32 trees of 64 nodes over 16k 528 for 504.
-  static constexpr float kBias = 7.f;
-  static constexpr float kRescale = 4.f;
+  static constexpr uint32_t kSums = (kApart ? 3 : 1) * N;  // columns of O^T for 128 value elements
+  static constexpr uint32_t kColS = 4 * kSums;             // S^T, twice 2 N
+  static constexpr uint32_t kTmem = kColS + 4 * N;
+  // log2 of the largest weight when the running maximum has moved, and how far a score may pass it (fp16 and E5M2 end
+  // behind 2^15).  Codes end at 2^-16, half a step off: 2^-28 of the largest at N = 64.  9 and 6 there move the maximum less
+  // often, 4,000 clocks each, but end at 2^-26: 16 x 4 positions of 128 heads over 8k 80 us for 85, a windowed chunk of 2,048
+  // tokens 194 for 201, 32 trees of 64 nodes over 16k 590 for 598.
+  static constexpr float kBias = kApart ? 9.f : 11.f;
+  static constexpr float kRescale = 15.f - kBias;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
   static_assert(kRingOff % 1024 == 0 && kRopeOff % 1024 == 0 && kPOff % 1024 == 0 && kBarOff % 8 == 0,
                 "swizzled tiles sit on 1 KB boundaries");
@@ -146,14 +161,23 @@ __device__ __forceinline__ void tma_rope(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(0), "r"(row), "r"(block), "r"(smem_u32(bar))
       : "memory");
 }
-// Two weights -> hi + lo: the E5M2 code is the high byte of fp16, rounded to nearest; what is left goes to E4M3.
-// hi: bytes 1 and 3; lo: the low 16 bits.  A NaN is one in lo.
-__device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x, y);
-  const uint32_t b = *reinterpret_cast<const uint32_t*>(&h);
-  hi = (b + 0x00800080u) & 0xff00ff00u;
-  const __half2 rest = __hsub2(h, *reinterpret_cast<const __half2*>(&hi));
-  lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(rest), __NV_SATFINITE, __NV_E4M3);
+// Two weights (at most 2^15) -> three E5M2 codes, each to nearest, of what the ones before leave; `by`: 16 where mid and lo
+// have sums of their own, and count 2^-4 and 2^-8, else 1.  An E5M2 code is the high byte of fp16, and leaves at most an
+// eighth of the power of two below its value: exact in fp16, and times 16 no larger than that power.  hi, mid: bytes 1
+// and 3; lo: the low 16 bits.  A NaN is one in lo.
+__device__ __forceinline__ uint32_t high_code(__half2 h) {
+  return (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xff00ff00u;
+}
+template <int kBy>
+__device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y), by = __float2half2_rn((float)kBy);
+  hi = high_code(h);
+  __half2 rest = __hsub2(h, *reinterpret_cast<const __half2*>(&hi));
+  if (kBy != 1) rest = __hmul2(rest, by);
+  mid = high_code(rest);
+  rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&mid));
+  if (kBy != 1) rest = __hmul2(rest, by);
+  lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(rest), __NV_SATFINITE, __NV_E5M2);
 }
 
 // A load where `on`, else `other`, issued where it stands (an ordinary one is moved down to its use, a block later) and
@@ -166,7 +190,7 @@ __device__ __forceinline__ uint32_t load_if(bool on, const void* p, uint32_t oth
 }
 
 struct BarsF8 {
-  uint64_t q_full, p_full, o_step, o_done, o_free, fin;
+  uint64_t q_full, p_full, l_full, l_free, o_step, o_done, o_free, fin;
   uint64_t s_full[2], r_full[kMaxRopes], r_free[kMaxRopes], e_full[kMaxPairs], e_free[kMaxPairs];
   uint32_t tmem, abort;
   uint32_t dead[2][2];  // softmax: a warp of the half gave up, by parity of the barrier's count
@@ -213,6 +237,8 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
   if (tid == 0) {
     mbar_init(&B.q_full, kSoftThreads);
     mbar_init(&B.p_full, kSoftThreads);
+    mbar_init(&B.l_full, kSoftThreads);
+    mbar_init(&B.l_free, 1);
     mbar_init(&B.o_step, 1);
     mbar_init(&B.o_done, 1);
     mbar_init(&B.o_free, kSoftThreads);
@@ -260,7 +286,7 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
     // ---- copies: lane l < 16 (and l + 16) holds the cache block and row of a block's run l (-1: not read): of this block,
     // and of the next one --------------------------------------------------------------------------
     const int run = maps.run, runs = kBlk / run;
-    int pairs = 0;  // filled, or being filled
+    int pairs = 0, ropes = 0;  // filled, or being filled
     bool ok = true;
     while (ok && walk.next(a, own, s)) {
       if (s.b0 >= s.b1) continue;
@@ -305,8 +331,13 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
         if (!ok) break;
         const int slot = g % C::kRopes, use = g / C::kRopes;
         if (use >= 1 && !wait(&B.r_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
+        // N = 64: the last codes of the weights lie there from the next block's S^T (a tile's last block: its own) to their
+        // part of O^T
+        const int under = b == s.b0 ? g - 1 : g - 2;
+        if (!C::kApart && under >= 0 && !wait(&B.l_free, (uint32_t)under)) { ok = false; break; }
         if (lane == 0) mbar_arrive_expect_tx(&B.r_full[slot], got * (uint32_t)run * 64u);
         __syncwarp();
+        ropes = g + 1;
         if (blk >= 0 && lane < 16)
           tma_rope(sb + C::kRopeOff + (uint32_t)slot * kRopeF8 + off * 64u, &maps.rope, in, blk, &B.r_full[slot]);
       }
@@ -316,7 +347,7 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
     bool landed = true;
     for (int x = max(0, pairs - C::kRing); x < pairs; ++x)
       landed = phase_wait(&B.e_full[x % C::kRing], (uint32_t)(x / C::kRing) & 1u, a.wait_ns) && landed;
-    for (int x = max(0, g - C::kRopes); x < g; ++x)  // (of the blocks whose rope keys were asked for)
+    for (int x = max(0, ropes - C::kRopes); x < ropes; ++x)
       landed = phase_wait(&B.r_full[x % C::kRopes], (uint32_t)(x / C::kRopes) & 1u, a.wait_ns) && landed;
     if (!landed) fail();
   } else if (warp == kMmaWarp) {
@@ -325,12 +356,13 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
     // The proxy fences stand here, behind the waits, for the bytes that other threads wrote with ordinary stores.
     const uint32_t el = elect();
     constexpr uint32_t kIdS = idesc8(false, 2 * N, false, false);
-    constexpr bool kMnP = N >= 32;  // P^T: [token][N rows], else [row][128 tokens]
-    constexpr uint32_t kIdHi = idesc8(true, N, true, kMnP), kIdLo = idesc8(false, N, true, kMnP);
+    constexpr bool kMnP = N >= 32;  // P^T of a code: [token][N rows], else [row][128 tokens]
+    constexpr uint32_t kIdO = idesc8(true, (int)C::kSums, true, kMnP);
     constexpr uint32_t kHighP = N == 64 ? kHigh64 : N == 32 ? kHigh32 : kHigh128;
     constexpr uint32_t kStepP = (kMnP ? 32u * N : 32u) >> 4;  // 32 tokens further
     const uint32_t ring = sdesc(sb + C::kRingOff, 16), rope = sdesc(sb + C::kRopeOff, 16);
-    const uint32_t qd = sdesc(sb, 16), qr = sdesc(sb + C::kQRopeOff, 16), pd = sdesc(sb + C::kPOff, 16);
+    const uint32_t qd = sdesc(sb, 16), qr = sdesc(sb + C::kQRopeOff, 16), ld = sdesc(sb + C::kLastOff, 16);
+    const uint32_t pd = sdesc(sb + C::kPOff, kMnP ? C::kPPart : 16);  // (N = 32: the three codes' columns, that far apart)
     bool ok = true, open = false, first = false, last = false;  // of the block whose O^T is to come
     int og = 0, otc = 0;
     auto value = [&]() -> bool {
@@ -338,22 +370,36 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
       if (first && otc >= 1 && !wait(&B.o_free, (uint32_t)(otc - 1))) return false;
       fence_proxy_async_smem();
       tc_after();
+      // chunk x (128 value elements) of the block's codes; 32 tokens kk of them
+      auto codes = [&](int x, int kk) -> uint32_t {
+        return ring + (((uint32_t)((kPairs * og + (x >> 1)) % C::kRing) * kPairF8 + (uint32_t)(x & 1) * kAtom +
+                        (uint32_t)kk * 8 * kAtom) >> 4);
+      };
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        const int slot = (kPairs * og + i) % C::kRing;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t d = tmem + (uint32_t)((2 * i + h) * N);
-          const uint32_t v = ring + (((uint32_t)slot * kPairF8 + (uint32_t)h * kAtom) >> 4);
+        for (int x = 2 * i; x < 2 * i + 2; ++x)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t at = v + ((uint32_t)kk * 8 * kAtom >> 4);
-            mma8<kHighPair, kHighP>(d, at, pd + kk * kStepP, kIdHi, (!first || kk > 0) ? 1u : 0u, el);
-            mma8<kHighPair, kHighP>(d, at, pd + (C::kPHalf >> 4) + kk * kStepP, kIdLo, 1u, el);
+            const uint32_t d = tmem + (uint32_t)x * C::kSums, at = codes(x, kk);
+            mma8<kHighPair, kHighP>(d, at, pd + kk * kStepP, kIdO, (!first || kk > 0) ? 1u : 0u, el);
+            if (!C::kApart) mma8<kHighPair, kHighP>(d, at, pd + (C::kPPart >> 4) + kk * kStepP, kIdO, 1u, el);
           }
+        if (!C::kApart) {  // the last codes come while these products run
+          if (i == 0) {
+            if (!wait(&B.l_full, (uint32_t)og)) return false;
+            fence_proxy_async_smem();
+            tc_after();
+          }
+#pragma unroll
+          for (int x = 2 * i; x < 2 * i + 2; ++x)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma8<kHighPair, kHighP>(tmem + (uint32_t)x * C::kSums, codes(x, kk), ld + kk * kStepP, kIdO, 1u, el);
         }
-        mma_commit(&B.e_free[slot], el);
+        mma_commit(&B.e_free[(kPairs * og + i) % C::kRing], el);
       }
+      if (!C::kApart) mma_commit(&B.l_free, el);
       mma_commit(&B.o_step, el);
       if (last) mma_commit(&B.o_done, el);
       return true;
@@ -631,7 +677,7 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
           }
           if (b > s.b0) {
 #pragma unroll 1
-            for (int i = 0; i < 4 && !dead; ++i) {
+            for (int i = 0; i < 4 * (int)C::kSums / N && !dead; ++i) {
 #pragma unroll
               for (int c = 0; c < NC; c += 8) {
                 float o[8];
@@ -647,34 +693,44 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
           named_sync(bar_half, 128);  // row_f is free
         }
         // weights
-        uint32_t hi[NC / 2], lo[NC / 2];
 #pragma unroll
-        for (int c = 0; c < NC; c += 2) {
-          v[c] = ex2(v[c]);
-          v[c + 1] = ex2(v[c + 1]);
-          split_weights(v[c], v[c + 1], hi[c / 2], lo[c / 2]);
-        }
+        for (int c = 0; c < NC; ++c) v[c] = ex2(v[c]);
+        constexpr int kBy = C::kApart ? 16 : 1;
+        uint4 last[(NC + 15) / 16];  // lo codes
         if constexpr (N == 16) {  // [row][128 tokens]
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const uint32_t to = swz(sb + C::kPOff, c0 + c, tok >> 4) + (uint32_t)(tok & 15);
-            st_u8(to, hi[c / 2] >> (c & 1 ? 24 : 8));
-            st_u8(to + C::kPHalf, lo[c / 2] >> (c & 1 ? 8 : 0));
+          for (int c = 0; c < NC; c += 2) {
+            uint32_t hi, mid, lo;
+            split_weights<kBy>(v[c], v[c + 1], hi, mid, lo);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t to = swz(sb + C::kPOff, c0 + c + k, tok >> 4) + (uint32_t)(tok & 15);
+              st_u8(to, hi >> (16 * k + 8));
+              st_u8(to + C::kPPart, mid >> (16 * k + 8));
+              st_u8(to + 2 * C::kPPart, lo >> (8 * k));
+            }
           }
         } else {  // [token][N rows]
 #pragma unroll
           for (int c = 0; c < NC; c += 16) {
-            uint32_t h[4], w[4];
+            uint32_t h[4], m[4], w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              h[k] = __byte_perm(hi[c / 2 + 2 * k], hi[c / 2 + 2 * k + 1], 0x7531);
-              w[k] = __byte_perm(lo[c / 2 + 2 * k], lo[c / 2 + 2 * k + 1], 0x5410);
+              uint32_t hi[2], mid[2], lo[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                split_weights<kBy>(v[c + 4 * k + 2 * x], v[c + 4 * k + 2 * x + 1], hi[x], mid[x], lo[x]);
+              h[k] = __byte_perm(hi[0], hi[1], 0x7531);
+              m[k] = __byte_perm(mid[0], mid[1], 0x7531);
+              w[k] = __byte_perm(lo[0], lo[1], 0x5410);
             }
             const int chunk = (c0 + c) / 16;
             const uint32_t to = N == 64 ? swz64(sb + C::kPOff, tok, chunk) : swz32(sb + C::kPOff, tok, chunk);
             st_v4(to, make_uint4(h[0], h[1], h[2], h[3]));
-            st_v4(to + C::kPHalf, make_uint4(w[0], w[1], w[2], w[3]));
+            st_v4(to + C::kPPart, make_uint4(m[0], m[1], m[2], m[3]));
+            last[c / 16] = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          if (C::kApart) st_v4(swz32(sb + C::kLastOff, tok, hw), last[0]);
         }
         if (!plain) {
           // A weight of 0 times a code that is NaN would be NaN: such codes of rows that a position of the tile does not
@@ -705,6 +761,14 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
           const float2 y = __ffma2_rn(make_float2(v[c], v[c + 1]), make_float2(unscale, unscale), make_float2(l[c], l[c + 1]));
           l[c] = y.x;
           l[c + 1] = y.y;
+        }
+        if constexpr (!C::kApart) {
+          // over the rope keys: behind the next block's S^T if it is of this tile (the next tile's are not asked for before
+          // this block's O^T)
+          if (b + 1 < s.b1) dead = dead || !wait(&B.s_full[(g + 1) & 1], (uint32_t)((g + 1) >> 1));
+#pragma unroll
+          for (int c = 0; c < NC; c += 16) st_v4(swz64(sb + C::kLastOff, tok, (c0 + c) / 16), last[c / 16]);
+          mbar_arrive(&B.l_full);
         }
         if (b == s.b0) advance();  // (while these warps have time)
       }
@@ -745,8 +809,18 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < 4 && !dead; ++i) {
         float o[NC];
-        tmem_ld<NC>(tmem + lane_addr + (uint32_t)(i * N + c0), o);
-        tmem_wait_ld();
+        const uint32_t from = tmem + lane_addr + (uint32_t)i * C::kSums + (uint32_t)c0;
+        tmem_ld<NC>(from, o);
+        if constexpr (C::kApart) {
+          float mid[NC], lo[NC];
+          tmem_ld<NC>(from + N, mid);
+          tmem_ld<NC>(from + 2 * N, lo);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < NC; ++c) o[c] += 0.0625f * (mid[c] + 0.0625f * lo[c]);
+        } else {
+          tmem_wait_ld();
+        }
         const int e = i * 128 + tok;  // value element
         if (s.part >= 0) {
           float* dst = a.part_o + (((int64_t)blockIdx.x * 2 + s.part) * N + c0) * kVal + e;
