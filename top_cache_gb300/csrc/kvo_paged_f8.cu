@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   if (sb & 1023u) {  // there is no room to align it here: nothing is computed, and nothing joined
+    grid_wait();     // (the list's launch writes both)
     if (threadIdx.x == 0 && blockIdx.x == 0) {
       *a.status = kErrPlan;
       a.head[kHdListed] = 0;
