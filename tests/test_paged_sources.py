@@ -28,3 +28,8 @@ def test_nothing_is_reported_while_the_launch_before_may_still_write(file, name,
     # the kernel before it in the stream writes the status and the list's head too, and may come last
     early = text[:text.index("grid_wait();")]
     assert not re.search(r"\*a\.status\s*=|a\.head\[\w+\]\s*=(?!=)", early), "%s: %s" % (file, name)
+
+
+def test_a_join_that_may_meet_more_parts_than_it_holds_does_not_compile():
+    with open(os.path.join(build.CSRC, "kvo_paged_attend.cu")) as f:
+        assert re.search(r"static_assert\(kMaxWorkers <= kJoinParts,", f.read())

@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) schedule_paged_kernel(PagedAttendArg
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = kJoinWarps * 32;
 constexpr int kJoinParts = 256;  // most parts of a row
+static_assert(kMaxWorkers <= kJoinParts, "a tile has a part of every CTA at most");
 
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) join_paged_kernel(PagedAttendArgs a, float bias) {
