@@ -33,19 +33,23 @@
 // softmax of one block runs beside the products of another.  At N = 64 shared
 // memory has no room for the third codes: they lie where the next block's rope
 // keys have been, between its S^T and their part of O^T, and come behind an
-// arrival of their own while the first two run (596 us over 32 trees of 64 nodes of
-// 16k; behind one arrival 638).  Every wait is bounded, as there.
+// arrival of their own while the first two run (597 us over 32 trees of 64 nodes of
+// 16k; behind one arrival 638).  A block's rope keys are loaded and used between its
+// pairs, and the third codes' products come before the second pair's others, so that
+// their place is free early (4,690 clocks a block; rope keys last 4,890).  Every wait
+// is bounded, as there.
 //
 // What bounds it.  N = 16: HBM, 32 ragged requests of 64k, 16 heads, in 136 us
 // (6.4 TB/s, 0.93 of the copy rate; with what joins them 143).  The cache's bytes
 // are all it reads (ncu: 863 of 862 MB).  Two loads a token stand in the way, its
 // table entry and its scale: they are made two blocks and one block ahead and
-// the scales are fetched into L2 with the codes (157 us before).  N = 64: 4,900
+// the scales are fetched into L2 with the codes (157 us before).  N = 64: 4,700
 // clocks a block of 128 tokens.  The products take 1,200 (S^T, 18 of 64 to 78
-// clocks) and 2,400 to 3,300 (O^T, 48 of 50 to 69), and the next block's last slabs
-// and rope keys come some 900 after the last of them; the softmax, 3,500, runs
-// beside.  (With two codes 4,200.  The 16-bit kernel takes 4,800 and the 4-bit one
-// 6,200.)  Borders of tiles cost 10,000: the queries 3,000 to 4,000, the output or
+// clocks) and 2,400 to 3,300 (O^T, 48 of 50 to 69), and their warp waits 750 for the
+// next block's codes, whose places the last products free, 240 for its rope keys and
+// 440 for weights; the softmax, 3,500, runs beside.  (With two codes 4,200.  The
+// 16-bit kernel takes 4,800 and the 4-bit one 6,200.)  These kernels spill 24 to 28
+// bytes a thread at 168 registers.  Borders of tiles cost 10,000: the queries 3,000 to 4,000, the output or
 // the parts 4,000 to 6,000 (64 rows of 2 KB).
 // Tried and not faster: four warps of their own for the queries (a latency of
 // memory a row: 106 us for 82 over 16 x 4 positions of 128 heads of 8k), votes on
@@ -321,6 +325,19 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
         const uint32_t off = (uint32_t)((lane & 15) * run);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
+          if (i == 1) {  // the rope keys, which the products take between the pairs
+            const int slot = g % C::kRopes, use = g / C::kRopes;
+            if (use >= 1 && !wait(&B.r_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
+            // N = 64: the last codes of the weights lie there from the next block's S^T (a tile's last block: its own) to
+            // their part of O^T
+            const int under = b == s.b0 ? g - 1 : g - 2;
+            if (!C::kApart && under >= 0 && !wait(&B.l_free, (uint32_t)under)) { ok = false; break; }
+            if (lane == 0) mbar_arrive_expect_tx(&B.r_full[slot], got * (uint32_t)run * 64u);
+            __syncwarp();
+            ropes = g + 1;
+            if (blk >= 0 && lane < 16)
+              tma_rope(sb + C::kRopeOff + (uint32_t)slot * kRopeF8 + off * 64u, &maps.rope, in, blk, &B.r_full[slot]);
+          }
           const int x = kPairs * g + i, slot = x % C::kRing, use = x / C::kRing;
           if (use >= 1 && !wait(&B.e_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
           if (lane == 0) mbar_arrive_expect_tx(&B.e_full[slot], got * (uint32_t)run * 256u);
@@ -330,17 +347,6 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
             tma_codes(sb + C::kRingOff + (uint32_t)slot * kPairF8 + off * 256u, &maps.codes, 2 * i, in >> 3, blk, &B.e_full[slot]);
         }
         if (!ok) break;
-        const int slot = g % C::kRopes, use = g / C::kRopes;
-        if (use >= 1 && !wait(&B.r_free[slot], (uint32_t)(use - 1))) { ok = false; break; }
-        // N = 64: the last codes of the weights lie there from the next block's S^T (a tile's last block: its own) to their
-        // part of O^T
-        const int under = b == s.b0 ? g - 1 : g - 2;
-        if (!C::kApart && under >= 0 && !wait(&B.l_free, (uint32_t)under)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(&B.r_full[slot], got * (uint32_t)run * 64u);
-        __syncwarp();
-        ropes = g + 1;
-        if (blk >= 0 && lane < 16)
-          tma_rope(sb + C::kRopeOff + (uint32_t)slot * kRopeF8 + off * 64u, &maps.rope, in, blk, &B.r_full[slot]);
       }
     }
     if (!ok) fail();
@@ -377,30 +383,29 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
                         (uint32_t)kk * 8 * kAtom) >> 4);
       };
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
+      for (int x = 0; x < 4; ++x) {
 #pragma unroll
-        for (int x = 2 * i; x < 2 * i + 2; ++x)
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t d = tmem + (uint32_t)x * C::kSums, at = codes(x, kk);
+          mma8<kHighPair, kHighP>(d, at, pd + kk * kStepP, kIdO, (!first || kk > 0 || (!C::kApart && x >= 2)) ? 1u : 0u, el);
+          if (!C::kApart) mma8<kHighPair, kHighP>(d, at, pd + (C::kPPart >> 4) + kk * kStepP, kIdO, 1u, el);
+        }
+        if (!C::kApart && x == 1) {
+          // the last codes come while these products run, and all their products before the other pair's: the next rope
+          // keys wait for their place
+          if (!wait(&B.l_full, (uint32_t)og)) return false;
+          fence_proxy_async_smem();
+          tc_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t d = tmem + (uint32_t)x * C::kSums, at = codes(x, kk);
-            mma8<kHighPair, kHighP>(d, at, pd + kk * kStepP, kIdO, (!first || kk > 0) ? 1u : 0u, el);
-            if (!C::kApart) mma8<kHighPair, kHighP>(d, at, pd + (C::kPPart >> 4) + kk * kStepP, kIdO, 1u, el);
-          }
-        if (!C::kApart) {  // the last codes come while these products run
-          if (i == 0) {
-            if (!wait(&B.l_full, (uint32_t)og)) return false;
-            fence_proxy_async_smem();
-            tc_after();
-          }
-#pragma unroll
-          for (int x = 2 * i; x < 2 * i + 2; ++x)
+          for (int y = 0; y < 4; ++y)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma8<kHighPair, kHighP>(tmem + (uint32_t)x * C::kSums, codes(x, kk), ld + kk * kStepP, kIdO, 1u, el);
+              mma8<kHighPair, kHighP>(tmem + (uint32_t)y * C::kSums, codes(y, kk), ld + kk * kStepP, kIdO,
+                                      (!first || y < 2 || kk > 0) ? 1u : 0u, el);
+          mma_commit(&B.l_free, el);
         }
-        mma_commit(&B.e_free[(kPairs * og + i) % C::kRing], el);
+        if (x & 1) mma_commit(&B.e_free[(kPairs * og + (x >> 1)) % C::kRing], el);
       }
-      if (!C::kApart) mma_commit(&B.l_free, el);
       mma_commit(&B.o_step, el);
       if (last) mma_commit(&B.o_done, el);
       return true;
@@ -412,6 +417,15 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
         const uint32_t dS = tmem + C::kColS + (uint32_t)(g & 1) * (2 * N);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
+          if (i == 1) {
+            const int slot = g % C::kRopes;
+            if (!wait(&B.r_full[slot], (uint32_t)(g / C::kRopes))) { ok = false; break; }
+            tc_after();
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+              mma8<kHigh64, kHigh64>(dS, rope + ((uint32_t)slot * kRopeF8 >> 4) + (uint32_t)(kk * 2), qr + (uint32_t)(kk * 2), kIdS, 1u, el);
+            mma_commit(&B.r_free[slot], el);
+          }
           const int x = kPairs * g + i, slot = x % C::kRing, use = x / C::kRing;
           if (!wait(&B.e_full[slot], (uint32_t)use)) { ok = false; break; }
           fence_proxy_async_smem();
@@ -422,14 +436,8 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
                 dS, ring + (((uint32_t)slot * kPairF8 + (uint32_t)(kk >> 2) * kAtom) >> 4) + (uint32_t)((kk & 3) * 2),
                 qd + (((uint32_t)(2 * i + (kk >> 2)) * C::kQSlab) >> 4) + (uint32_t)((kk & 3) * 2), kIdS, (i | kk) ? 1u : 0u, el);
         }
-        const int slot = g % C::kRopes;
-        if (!ok || !wait(&B.r_full[slot], (uint32_t)(g / C::kRopes))) { ok = false; break; }
-        tc_after();
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-          mma8<kHigh64, kHigh64>(dS, rope + ((uint32_t)slot * kRopeF8 >> 4) + (uint32_t)(kk * 2), qr + (uint32_t)(kk * 2), kIdS, 1u, el);
+        if (!ok) break;
         mma_commit(&B.s_full[g & 1], el);
-        mma_commit(&B.r_free[slot], el);
         if (open && !value()) { ok = false; break; }
         open = true;
         first = b == s.b0;
