@@ -589,8 +589,17 @@ int kvo_paged_attend(const void* pool, int64_t n_blocks, int32_t block_tokens, i
  *   kvo_paged_plan (window 0, every request n_r >= 0), kvo_tree_masks;
  *   for each layer kvo_paged_write, kvo_paged_attend_tree;
  *   kvo_tree_accept, kvo_paged_commit, kvo_paged_move
- * and may be captured into one graph.  A request that ends, does so in a plan
- * of its own, with the window.  At most 1024 nodes a request.
+ * and may be captured into one graph.  At most 1024 nodes a request.
+ *   A request that ends, does so in a plan of its own, with the window: with window
+ *   0 its plan would free again the blocks that kvo_paged_commit has, unnoticed, and
+ *   two requests would then share one.
+ *   Requests with a prompt chunk go in a step of their own (kvo_paged_plan,
+ *   kvo_paged_write, kvo_paged_attend): to kvo_tree_accept a chunk's tokens are
+ *   drafts, of which it keeps those that the model would have chosen.
+ *   kvo_tree_accept accepts by equality of tokens.  For another rule the caller
+ *   writes path and accepted itself; commit and move take any.
+ *   The handle's layers (kvo_append, kvo_step, kvo_attend) take the positions of a
+ *   step as a chain of at most 8: a model that has them cannot verify a tree.
  * ------------------------------------------------------------------------ */
 
 /*
