@@ -122,3 +122,29 @@ def test_the_check_sees_weights_of_eight_bits():
     for held, fine in ((code(w, 7, -133, 3e38), True), (hi + code(w - hi, 3, -9, 448.0), False)):
         ref, got = w @ v, held @ v
         assert (np.linalg.norm(got - ref) / np.linalg.norm(ref) <= LIMIT) == fine
+
+
+@pytest.mark.parametrize("H", [16, 32, 64])
+def test_scores_whose_steps_pass_the_weights_range(H):
+    # log2 scores of 2^22 to 2^36: steps of 1 to 2^13 between fp32 numbers, so the running maximum and what is added to it
+    # round to each other.  Scores are off by at most 2^-22 of 576 products: where the largest is ahead by more, the output
+    # is its row, rounded to bf16.
+    lens = [600, 129]
+    c = Cache(lens, 16, F8, 21)
+    x = np.random.default_rng(22).standard_normal((2, H, 576))
+    for power in range(20, 34):
+        q_bits = O.bf16_bits(x * 2.0 ** power)
+        out, lse = attend(c, q_bits, [0, 1, 2], lens)
+        got, q = O.bf16_values(out), O.bf16_values(q_bits)
+        assert np.isfinite(got).all() and np.isfinite(lse).all(), "scores of 2^%d" % (power + 2)
+        sure = 0
+        for r, n in enumerate(lens):
+            k, _ = c.rows_of(r)(np.arange(n))
+            z = SCALE * (q[r] @ k.T)
+            off = 2.0 ** -22 * 576 * SCALE * (np.abs(q[r]) @ np.abs(k).T).max(-1)
+            two = np.sort(z, -1)[:, -2:]
+            ahead = two[:, 1] - two[:, 0] > 2 * off + 30
+            top = k[z.argmax(-1)][:, :512]
+            assert (np.abs(got[r] - top) <= 2.0 ** -8 * np.abs(top))[ahead].all(), "scores of 2^%d" % (power + 2)
+            sure += ahead.sum()
+        assert sure > H

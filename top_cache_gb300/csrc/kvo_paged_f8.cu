@@ -673,10 +673,12 @@ __global__ void __launch_bounds__(ShapeF8<N>::kThreads, 1)
           named_sync(bar_half, 128);
           if (quad == 0 && lane < NC) {
             const float* wm = warp_red + 4 * hw * NC + lane;
-            const float old = C::kBias - less_max[c0 + lane];
-            const float now = fmaxf(old, fmaxf(fmaxf(wm[0], wm[NC]), fmaxf(wm[2 * NC], wm[3 * NC])));
-            less_max[c0 + lane] = C::kBias - now;
-            row_f[c0 + lane] = ex2(old - now);
+            const float top = fmaxf(fmaxf(wm[0], wm[NC]), fmaxf(wm[2 * NC], wm[3 * NC])), old = less_max[c0 + lane];
+            // (far from 0, kBias - top may round to 16 - top, and 2^16 is past the weights' range)
+            float less = fminf(old, C::kBias - top);
+            if (less + top > C::kBias + C::kRescale) less = -top;
+            less_max[c0 + lane] = less;
+            row_f[c0 + lane] = ex2(less - old);
           }
           named_sync(bar_half, 128);
 #pragma unroll
