@@ -49,8 +49,8 @@
 // next block's codes, whose places the last products free, 240 for its rope keys and
 // 440 for weights; the softmax, 3,500, runs beside.  (With two codes 4,200.  The
 // 16-bit kernel takes 4,800 and the 4-bit one 6,200.)  These kernels spill 24 to 28
-// bytes a thread at 168 registers.  Borders of tiles cost 10,000: the queries 3,000 to 4,000, the output or
-// the parts 4,000 to 6,000 (64 rows of 2 KB).
+// bytes a thread at 168 registers.  Borders of tiles cost 10,000: the queries 3,000
+// to 4,000, the output or the parts 4,000 to 6,000 (64 rows of 2 KB).
 // Tried and not faster: four warps of their own for the queries (a latency of
 // memory a row: 106 us for 82 over 16 x 4 positions of 128 heads of 8k), votes on
 // the running maximum counted behind the weights (73 for 70), 32 columns of TMEM a
@@ -165,7 +165,7 @@ __device__ __forceinline__ void tma_rope(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(0), "r"(row), "r"(block), "r"(smem_u32(bar))
       : "memory");
 }
-// Two weights (at most 2^15) -> three E5M2 codes, each to nearest, of what the ones before leave; `by`: 16 where mid and lo
+// Two weights (at most 2^15) -> three E5M2 codes, each to nearest, of what the ones before leave; kBy: 16 where mid and lo
 // have sums of their own, and count 2^-4 and 2^-8, else 1.  An E5M2 code is the high byte of fp16, and leaves at most an
 // eighth of the power of two below its value: exact in fp16, and times 16 no larger than that power.  hi, mid: bytes 1
 // and 3; lo: the low 16 bits.  A NaN is one in lo.
